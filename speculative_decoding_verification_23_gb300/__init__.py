@@ -324,3 +324,12 @@ def spec_tv_budget(args: SpecArgs, *, device=None, workspace=None, stream=None, 
         raise SpecError(rc, "spec_tv_budget")
     k = args.total_drafts
     return tv[:k], theta[:k], (px[:k] if px is not None else None), (qx[:k] if qx is not None else None)
+
+
+from .tree import (  # noqa: E402,F401  (the drafted-tree operators use the helpers above)
+    EXPORTED_TREE, SPEC_F16, SPEC_MAX_BEAMS, SPEC_MAX_STATES, SPEC_MAX_TREE, SPEC_STATUS_BAD_LEN,
+    SPEC_STATUS_BAD_PAGE, SpecBeamArgs, SpecBeamState, SpecCache, SpecCommitArgs, SpecEvictArgs, SpecTreeArgs,
+    SpecWeighArgs, make_beam_args, make_beam_workspace, make_cache, make_commit_args, make_evict_args,
+    make_reorder_args, make_tree_args, make_tree_workspace, make_weigh_args, spec_attention_weights,
+    spec_beam_reorder, spec_beam_select, spec_beam_workspace_bytes, spec_cache_commit, spec_cache_evict,
+    spec_tree_attention, spec_tree_workspace_bytes)

@@ -1,0 +1,228 @@
+// Eviction from a paged cache (selection, then the move) and commitment of
+// an accepted path: copies of whole key and value rows by 16-byte pieces.
+#include "tree_common.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelPer = 16;  // consecutive tokens per thread in the ordered pass
+
+// A weight's order as an unsigned integer: larger is better, NaN the worst.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0u;
+  const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ bool evict_bad_pages(const int32_t* row, long long tokens, int page_size, int num_pages) {
+  int bad = 0;
+  for (long long p = threadIdx.x; p < (tokens + page_size - 1) / page_size; p += blockDim.x) {
+    const int id = row[p];
+    bad |= id < 0 || id >= num_pages;
+  }
+  return __syncthreads_or(bad) != 0;
+}
+
+// One CTA per (request, head).  A radix select over the weights' order keys
+// (11, 11 and 10 bits) finds the key of the last kept token and how many of
+// its equals are kept; a pass in token order then writes the kept positions.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams P) {
+  __shared__ int hist[2048];
+  __shared__ int warp_tot[kSelThreads / 32];
+  __shared__ unsigned long long warp_tot2[kSelThreads / 32];
+  __shared__ int pick[2];
+  const int h = blockIdx.x % P.heads, b = blockIdx.x / P.heads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int len = P.len[b];
+  bool ok = len >= 0 && len <= P.ld && (long long)len <= (long long)P.ld_table * P.page_size;
+  const int m = ok ? min(len, P.keep) : 0;
+  bool page_bad = false;
+  if (ok) {
+    page_bad = evict_bad_pages(P.table + (long long)b * P.ld_table, len, P.page_size, P.num_pages);
+    page_bad = evict_bad_pages(P.to + (long long)b * P.ld_to, m, P.page_size, P.num_pages) || page_bad;
+  }
+  int32_t* index = P.index + ((long long)b * P.heads + h) * P.keep;
+  float* kept = P.kept ? P.kept + ((long long)b * P.heads + h) * P.keep : nullptr;
+  if (h == 0 && tid == 0) {
+    if (P.status) P.status[b] = !ok ? kStatusBadLen : (page_bad ? kStatusBadPage : 0);
+    P.new_len[b] = ok && !page_bad ? m : -1;
+  }
+  ok = ok && !page_bad;
+  for (int i = (ok ? m : 0) + tid; i < P.keep; i += kSelThreads) {
+    index[i] = -1;
+    if (kept) kept[i] = 0.f;
+  }
+  if (!ok) return;
+  const float* w = P.weights + ((long long)b * P.heads + h) * P.ld;
+  const bool all = len <= P.keep;
+  const int lo = P.sink, hi = len - P.recent;  // chosen by weight: [lo, hi)
+  int need = P.keep - P.sink - P.recent;       // of them (not for `all`)
+  uint32_t prefix = 0;                         // the last kept key so far
+  if (!all && need > 0) {
+    int shift = 32;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int bits = pass < 2 ? 11 : 10;
+      const int above = shift;  // bits fixed: [above, 32)
+      shift -= bits;
+      for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      for (int j = lo + tid; j < hi; j += kSelThreads) {
+        const uint32_t k = weight_key(w[j]);
+        if (above == 32 || (k >> above) == (prefix >> above)) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
+      }
+      __syncthreads();
+      // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t
+      const int x = hist[2047 - 2 * tid], y = hist[2046 - 2 * tid];
+      int v = x + y;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+      }
+      if (lane == 31) warp_tot[warp] = v;
+      __syncthreads();
+      int base = 0;
+      for (int i = 0; i < warp; ++i) base += warp_tot[i];
+      const int incl = base + v, excl = incl - x - y;
+      if (excl < need && incl >= need) {  // one thread
+        const bool first = excl + x >= need;
+        pick[0] = first ? 2047 - 2 * tid : 2046 - 2 * tid;
+        pick[1] = need - (first ? excl : excl + x);
+      }
+      __syncthreads();
+      prefix |= (uint32_t)pick[0] << shift;
+      need = pick[1];
+      __syncthreads();
+    }
+  }
+  // `need` tokens of key `prefix` (the first ones) and all above it
+  unsigned long long done = 0;  // kept without ties, ties (32 bits each)
+  for (int base = 0; base < len; base += kSelThreads * kSelPer) {
+    const int j0 = base + tid * kSelPer;
+    uint32_t sure = 0, tie = 0;
+#pragma unroll
+    for (int e = 0; e < kSelPer; ++e) {
+      const int j = j0 + e;
+      if (j >= len) break;
+      if (all || j < lo || j >= hi) {
+        sure |= 1u << e;
+      } else if (P.keep > P.sink + P.recent) {
+        const uint32_t k = weight_key(w[j]);
+        if (k > prefix) sure |= 1u << e;
+        if (k == prefix) tie |= 1u << e;
+      }
+    }
+    unsigned long long v = ((unsigned long long)__popc(sure) << 32) | (unsigned)__popc(tie);
+    const unsigned long long mine = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long t = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += t;
+    }
+    if (lane == 31) warp_tot2[warp] = v;
+    __syncthreads();
+    unsigned long long at = done + v - mine, sum = 0;
+    for (int i = 0; i < kSelThreads / 32; ++i) {
+      if (i < warp) at += warp_tot2[i];
+      sum += warp_tot2[i];
+    }
+    done += sum;
+    int ns = (int)(at >> 32), nt = (int)(at & 0xffffffffu);
+    for (int e = 0; e < kSelPer; ++e) {
+      const bool s = (sure >> e) & 1u, t = (tie >> e) & 1u;
+      if (s || (t && nt < need)) {
+        const int to = ns + min(nt, need);
+        index[to] = j0 + e;
+        if (kept) kept[to] = w[j0 + e];
+      }
+      ns += s;
+      nt += t;
+    }
+    __syncthreads();
+  }
+}
+
+// The move: 16-byte pieces of key and value rows, one kept token of a head
+// per `pieces` lanes.
+constexpr int kMoveThreads = 256;
+
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams P, int blocks) {
+  const int part = blockIdx.x % blocks, bh = blockIdx.x / blocks;
+  const int h = bh % P.heads, b = bh / P.heads;
+  const int m = P.new_len[b];
+  const int pieces = P.dim / 8, per = kMoveThreads / pieces;
+  const int i = part * per + (int)threadIdx.x / pieces, ch = threadIdx.x % pieces;
+  if (i >= m || (int)threadIdx.x >= per * pieces) return;
+  const int j = P.index[((long long)b * P.heads + h) * P.keep + i];
+  const PageDiv pd(P.page_size);
+  int ps, ss, pt, st;
+  pd.split(j, ps, ss);
+  pd.split(i, pt, st);
+  const long long from = (long long)P.table[(long long)b * P.ld_table + ps] * P.s_page + (long long)ss * P.s_slot +
+                         (long long)h * P.s_head + ch * 8;
+  const long long to = (long long)P.to[(long long)b * P.ld_to + pt] * P.s_page + (long long)st * P.s_slot +
+                       (long long)h * P.s_head + ch * 8;
+  const uint4 k = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.k) + from);
+  const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.v) + from);
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.k) + to) = k;
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.v) + to) = v;
+}
+
+// One CTA per (request, layer): checks the request, then copies its path.
+__global__ void __launch_bounds__(kMoveThreads) commit_kernel(const CommitParams P) {
+  const int b = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x;
+  const int cu = P.cu[b], n = P.cu[b + 1] - cu, m = P.path_len[b], ctx = P.ctx[b];
+  bool ok = cu >= 0 && n >= 0 && (long long)cu + n <= P.total && m >= 0 && m <= P.ld_path && ctx >= 0 &&
+            (long long)ctx + m <= (long long)P.ld_table * P.page_size;
+  const PageDiv pd(P.page_size);
+  const int32_t* path = P.path + (long long)b * P.ld_path;
+  const int32_t* table = P.table + (long long)b * P.ld_table;
+  int bad = 0;
+  if (ok)
+    for (int i = tid; i < m; i += kMoveThreads) {
+      int page, slot;
+      pd.split(ctx + i, page, slot);
+      const int node = path[i], id = table[page];
+      bad |= (node < 0 || node >= n ? 1 : 0) | (id < 0 || id >= P.num_pages ? 2 : 0);
+    }
+  const bool bad_node = __syncthreads_or(bad & 1) != 0, bad_page = __syncthreads_or(bad & 2) != 0;
+  if (layer == 0 && tid == 0) {
+    const int st = (!ok || bad_node ? kStatusBadLen : 0) | (bad_page ? kStatusBadPage : 0);
+    if (P.status) P.status[b] = st;
+    P.new_len[b] = st ? -1 : ctx + m;
+  }
+  if (!ok || bad_node || bad_page) return;
+  const int pieces = P.dim / 8, per_tok = P.heads * pieces;
+  for (int x = tid; x < m * per_tok; x += kMoveThreads) {
+    const int i = x / per_tok, y = x - i * per_tok, h = y / pieces, ch = y - h * pieces;
+    int page, slot;
+    pd.split(ctx + i, page, slot);
+    const long long from = (long long)layer * P.sn_layer + (long long)(cu + path[i]) * P.sn_node +
+                           (long long)h * P.sn_head + ch * 8;
+    const long long to = (long long)layer * P.s_layer + (long long)table[page] * P.s_page +
+                         (long long)slot * P.s_slot + (long long)h * P.s_head + ch * 8;
+    const uint4 k = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.k_new) + from);
+    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.v_new) + from);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.k) + to) = k;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.v) + to) = v;
+  }
+}
+
+}  // namespace
+
+int launch_evict(const EvictParams& P, cudaStream_t s) {
+  evict_select_kernel<<<P.B * P.heads, kSelThreads, 0, s>>>(P);
+  if (cudaGetLastError() != cudaSuccess) return -1;
+  const int per = kMoveThreads / (P.dim / 8), blocks = (P.keep + per - 1) / per;
+  evict_move_kernel<<<(unsigned)((long long)P.B * P.heads * blocks), kMoveThreads, 0, s>>>(P, blocks);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+int launch_commit(const CommitParams& P, cudaStream_t s) {
+  commit_kernel<<<dim3(P.B, P.layers), kMoveThreads, 0, s>>>(P);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace sv
