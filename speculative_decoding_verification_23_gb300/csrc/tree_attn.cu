@@ -311,7 +311,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
       }
     }
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) P.status[b] = r.ok ? (bad ? kStatusBadPage : 0) : kStatusBadLen;
+    int late = 0;
+    if (P.failed)
+      for (int c = threadIdx.x; c < P.grid; c += kJoinWarps * 32) late |= P.failed[c];
+    late = __syncthreads_or(late);
+    if (threadIdx.x == 0)
+      P.status[b] = (r.ok ? (bad ? kStatusBadPage : 0) : kStatusBadLen) | (late ? kStatusTimeout : 0);
   }
   const long long T_ = P.start[P.B], s0 = P.start[b];
   const bool range = r.cu >= 0 && r.n >= 0 && (long long)r.cu + r.n <= P.total;
@@ -393,9 +398,6 @@ TreePlan plan_tree_warp(int dim, int num_sms) {
   p.rows = 16;
   p.kt = kWtKeys;
   p.grid = num_sms * (dim <= 128 ? 2 : 1);
-  p.smem = dim == 64 ? WtShape<64>::kSmem
-                     : dim == 96 ? WtShape<96>::kSmem
-                                 : dim == 128 ? WtShape<128>::kSmem : dim == 192 ? WtShape<192>::kSmem : WtShape<256>::kSmem;
   return p;
 }
 

@@ -33,6 +33,7 @@ struct TreeParams {
   int32_t* status; // or null
   float* part_o;   // [2 * grid][rows][dim] unnormalised outputs of split items
   float2* part_ml; // [2 * grid][rows] their reference (log2 units) and sum
+  int32_t* failed; // [grid] whether a wait of a CTA ran out, or null
   long long* start;  // [B + 1] first tile of each request (main kernel to combine)
   float scale_log2;  // scale * log2(e)
   int B, total, max_nodes, mask_words, ld_table;
@@ -43,7 +44,7 @@ struct TreeParams {
 };
 
 struct TreeWorkspace {
-  size_t off_start, off_ml, off_o, total;
+  size_t off_start, off_failed, off_ml, off_o, total;
 };
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -51,7 +52,8 @@ inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 inline TreeWorkspace make_tree_workspace(int B, int grid, int rows, int dim) {
   TreeWorkspace w;
   w.off_start = 0;
-  w.off_ml = up256((size_t)(B + 1) * sizeof(long long));
+  w.off_failed = up256((size_t)(B + 1) * sizeof(long long));
+  w.off_ml = w.off_failed + up256((size_t)grid * sizeof(int32_t));
   w.off_o = w.off_ml + up256((size_t)2 * grid * rows * 2 * sizeof(float));
   w.total = w.off_o + up256((size_t)2 * grid * rows * dim * sizeof(float));
   return w;
@@ -59,8 +61,8 @@ inline TreeWorkspace make_tree_workspace(int B, int grid, int rows, int dim) {
 
 // How a call is run: the kernel, its grid, its rows per item and keys per tile.
 struct TreePlan {
-  int kernel;   // 0: warp tiles (tree_attn.cu)
-  int grid, rows, kt, smem;
+  int kernel;   // 0: warp tiles (tree_attn.cu), 1: tensor memory (tree_tc.cu)
+  int grid, rows, kt;
 };
 
 // ------------------------------------------------------- attention weights

@@ -15,6 +15,9 @@
 namespace sv {
 TreePlan plan_tree_warp(int dim, int num_sms);
 int launch_tree_warp(const TreeParams& P, bool bf16, cudaStream_t s);
+bool tree_tc_fits(int dim, int page_size);
+TreePlan plan_tree_tc(int rows, int num_sms);
+int launch_tree_tc(const TreeParams& P, bool bf16, cudaStream_t s);
 int launch_tree_join(const TreeParams& P, bool bf16, int num_sms, cudaStream_t s);
 int launch_weigh(const WeighParams& P, bool bf16, int num_sms, cudaStream_t s);
 int launch_evict(const EvictParams& P, cudaStream_t s);
@@ -88,7 +91,22 @@ int check_tree(const spec_tree_args* a) {
   return SPEC_OK;
 }
 
-sv::TreePlan plan_tree(const spec_tree_args* a, int num_sms) { return sv::plan_tree_warp(a->cache.dim, num_sms); }
+// A stride that a TMA copy takes along an axis of n elements.
+bool tma_stride(int64_t s, int64_t n) { return n == 1 || (s > 0 && s < (1ll << 38)); }
+
+// The tensor-memory kernel takes the calls whose tiles TMA can copy, with a
+// positive scale, and more query rows per key head than one warp tile holds.
+constexpr int kWarpRows = 16;
+
+sv::TreePlan plan_tree(const spec_tree_args* a, int num_sms) {
+  const spec_cache& c = a->cache;
+  const int rows = a->max_nodes * (a->heads_q / c.heads);
+  const bool fits = sv::tree_tc_fits(c.dim, c.page_size) && a->scale > 0.f && a->total_nodes > 0 &&
+                    tma_stride(c.s_slot, c.page_size) && tma_stride(c.s_head, c.heads) &&
+                    tma_stride(c.s_page, c.num_pages) && tma_stride(a->sn_node, a->total_nodes) &&
+                    tma_stride(a->sn_head, c.heads);
+  return fits && rows > kWarpRows ? sv::plan_tree_tc(rows, num_sms) : sv::plan_tree_warp(c.dim, num_sms);
+}
 
 uint16_t* layer_of(void* p, const spec_cache& c, int layer) {
   return static_cast<uint16_t*>(p) + (long long)layer * c.s_layer;
@@ -148,6 +166,7 @@ int spec_tree_attention(const spec_tree_args* a, void* out, int64_t so_node, int
   P.lse = out_lse;
   P.status = out_status;
   P.start = reinterpret_cast<long long*>(w + W.off_start);
+  P.failed = plan.kernel == 1 ? reinterpret_cast<int32_t*>(w + W.off_failed) : nullptr;
   P.part_ml = reinterpret_cast<float2*>(w + W.off_ml);
   P.part_o = reinterpret_cast<float*>(w + W.off_o);
   P.scale_log2 = a->scale * 1.4426950408889634f;
@@ -165,7 +184,7 @@ int spec_tree_attention(const spec_tree_args* a, void* out, int64_t so_node, int
   P.rows = plan.rows;
   P.kt = plan.kt;
   const bool bf16 = a->cache.dtype == SPEC_BF16;
-  if (sv::launch_tree_warp(P, bf16, s)) return SPEC_ERR_LAUNCH;
+  if (plan.kernel == 1 ? sv::launch_tree_tc(P, bf16, s) : sv::launch_tree_warp(P, bf16, s)) return SPEC_ERR_LAUNCH;
   return sv::launch_tree_join(P, bf16, sms, s) == 0 ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 
