@@ -40,13 +40,14 @@ __global__ void __launch_bounds__(kWtWarps * 32, WtShape<D>::kCtas) tree_warp_ke
   const T* vn = static_cast<const T*>(P.v_new);
   const T* q = static_cast<const T*>(P.q);
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const TreeScan scan = tree_scan(P, lane);
   if (blockIdx.x == 0 && warp == 0) tree_store_starts(P, scan, lane);
   TreeWalk walk;
   walk.begin(P, lane, scan, blockIdx.x);
   TreeSeg g;
   while (walk.next(P, g)) {
-    const TreeReq& r = g.r;
+    const TreeReq& r = walk.r;
     const int row_lo = g.m * 16;
     const int nrows = min(16, r.n * P.group - row_lo);
     // Q fragments, rows r0 and r0 + 8
@@ -284,23 +285,25 @@ __global__ void __launch_bounds__(kWtWarps * 32, WtShape<D>::kCtas) tree_warp_ke
         if (P.lse && d == 0)
           P.lse[(long long)(r.cu + nd) * P.heads * P.group + head] = L == 0.f ? -INFINITY : (R + log2f(L)) * kLn2;
       } else {
-        *reinterpret_cast<float2*>(P.part_o + ((long long)slot * 16 + row) * D + d) = make_float2(x, y);
+        *reinterpret_cast<float2*>(P.part_o + (((long long)slot * (D / 4) + d / 4) * 16 + row) * 4 + d % 4) = make_float2(x, y);
         if (d == 0) P.part_ml[(long long)slot * 16 + row] = make_float2(M, L);
       }
     }
   }
 }
 
-// Joins the pieces of split items: one warp per (node, head), with the
-// pieces in tile order.  Also the status of every request, and NaN in the
-// rows of a request whose lengths are bad.
-constexpr int kJoinWarps = 8;
+// Joins the pieces of split items, in tile order.  A warp takes 8 rows of one
+// item: lane l the row l % 8 and channels 4 (l / 8) .. + 3 of every 16, so
+// that pieces are read by 128 bytes and results written by 32.  Also the
+// status of every request, and NaN in the rows of one whose lengths are bad.
+constexpr int kJoinWarps = 4;
 
-template <typename T>
+template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeParams P) {
   const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const TreeReq r = tree_request(P, b);
   const int heads_q = P.heads * P.group;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.y == 0 && P.status) {
     int bad = 0;
     if (r.ok && r.n > 0) {
@@ -318,51 +321,65 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
     if (threadIdx.x == 0)
       P.status[b] = (r.ok ? (bad ? kStatusBadPage : 0) : kStatusBadLen) | (late ? kStatusTimeout : 0);
   }
-  const long long T_ = P.start[P.B], s0 = P.start[b];
-  const bool range = r.cu >= 0 && r.n >= 0 && (long long)r.cu + r.n <= P.total;
-  if (!range) return;
-  const long long nrow = (long long)r.n * heads_q;
-  for (long long i = (long long)blockIdx.y * kJoinWarps + warp; i < nrow; i += (long long)gridDim.y * kJoinWarps) {
-    const int node = (int)(i / heads_q), head = (int)(i - (long long)node * heads_q);
-    T* dst = static_cast<T*>(P.out) + (long long)(r.cu + node) * P.so_node + (long long)head * P.so_head;
-    float* lse = P.lse ? P.lse + (long long)(r.cu + node) * heads_q + head : nullptr;
-    if (!r.ok) {
-      for (int d = 2 * lane; d < P.dim; d += 64) *reinterpret_cast<uint32_t*>(dst + d) = pack2<T>(NAN, NAN);
-      if (lse && lane == 0) *lse = NAN;
-      continue;
+  if (r.cu < 0 || r.n < 0 || (long long)r.cu + r.n > P.total) return;
+  T* out = static_cast<T*>(P.out);
+  const int sub = lane & 7, quad = lane >> 3;
+  if (!r.ok) {
+    for (long long i = (long long)blockIdx.y * kJoinWarps + warp; i < (long long)r.n * heads_q;
+         i += (long long)gridDim.y * kJoinWarps) {
+      const int node = (int)(i / heads_q), head = (int)(i - (long long)node * heads_q);
+      T* dst = out + (long long)(r.cu + node) * P.so_node + (long long)head * P.so_head;
+      for (int d = 2 * lane; d < D; d += 64) *reinterpret_cast<uint32_t*>(dst + d) = pack2<T>(NAN, NAN);
+      if (P.lse && lane == 0) P.lse[(long long)(r.cu + node) * heads_q + head] = NAN;
     }
-    const int kvh = head / P.group, R = node * P.group + head % P.group;
-    const long long s = s0 + ((long long)kvh * r.mb + R / P.rows) * r.per_item;
-    const int used = tree_used(P, T_);
+    return;
+  }
+  const long long T_ = P.start[P.B], s0 = P.start[b];
+  const int used = tree_used(P, T_);
+  const int rows = r.n * P.group, blocks = (rows + 7) / 8;  // P.rows is a multiple of 8
+  for (int i = blockIdx.y * kJoinWarps + warp; i < blocks * P.heads; i += gridDim.y * kJoinWarps) {
+    const int kvh = i / blocks, R0 = (i - kvh * blocks) * 8;
+    const long long s = s0 + ((long long)kvh * r.mb + R0 / P.rows) * r.per_item;
     const int c0 = tree_owner(s, T_, used), c1 = tree_owner(s + r.per_item - 1, T_, used);
     if (c0 == c1) continue;  // written whole
-    const int row = R % P.rows;
-    // CTAs c0 (slot 1) and c0 + 1 .. c1 (slot 0)
-    auto part = [&](int c) { return ((long long)2 * c + (c == c0 ? 1 : 0)) * P.rows + row; };
+    const bool in = R0 + sub < rows;
+    const int row = R0 % P.rows + (in ? sub : 0);
+    // CTA c0 in slot 1, c0 + 1 .. c1 in slot 0
     float M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(&P.part_ml[part(c)]).x);
-    M = warp_max(M);
+    for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(&P.part_ml[(2ll * c + (c == c0)) * P.rows + row]).x);
     const float ref = M == -INFINITY ? 0.f : M;
     float L = 0.f;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-      const float2 v = __ldcg(&P.part_ml[part(c)]);
-      L += v.y * ex2(v.x - ref);
-    }
-    L = warp_sum(L);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    for (int d = 2 * lane; d < P.dim; d += 64) {
-      float x = 0.f, y = 0.f;
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const long long at = part(c);
-        const float f = ex2(__ldcg(&P.part_ml[at]).x - ref);
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(P.part_o + at * P.dim + d));
-        x += v.x * f;
-        y += v.y * f;
+    float4 acc[D / 16];
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; ++c) {
+      const long long at = 2ll * c + (c == c0);
+      const float2 ml = __ldcg(&P.part_ml[at * P.rows + row]);
+      const float f = ex2(ml.x - ref);
+      L += ml.y * f;
+      const float4* src = reinterpret_cast<const float4*>(P.part_o) + (at * (D / 4) + quad) * P.rows + row;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const float4 v = __ldcg(src + (long long)k * 4 * P.rows);
+        acc[k].x += v.x * f;
+        acc[k].y += v.y * f;
+        acc[k].z += v.z * f;
+        acc[k].w += v.w * f;
       }
-      *reinterpret_cast<uint32_t*>(dst + d) = pack2<T>(x * inv, y * inv);
     }
-    if (lse && lane == 0) *lse = L == 0.f ? -INFINITY : (ref + log2f(L)) * kLn2;
+    if (!in) continue;
+    const int R = R0 + sub, node = R / P.group, head = kvh * P.group + R - node * P.group;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    T* dst = out + (long long)(r.cu + node) * P.so_node + (long long)head * P.so_head + quad * 4;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      uint2 v;
+      v.x = pack2<T>(acc[k].x * inv, acc[k].y * inv);
+      v.y = pack2<T>(acc[k].z * inv, acc[k].w * inv);
+      *reinterpret_cast<uint2*>(dst + k * 16) = v;
+    }
+    if (P.lse && quad == 0)
+      P.lse[(long long)(r.cu + node) * heads_q + head] = L == 0.f ? -INFINITY : (ref + log2f(L)) * kLn2;
   }
 }
 
@@ -405,18 +422,45 @@ int launch_tree_warp(const TreeParams& P, bool bf16, cudaStream_t s) {
   return bf16 ? launch_warp_dim<__nv_bfloat16>(P, s) : launch_warp_dim<__half>(P, s);
 }
 
+namespace {
+template <typename T, int D>
+int launch_join(const TreeParams& P, int num_sms, cudaStream_t s) {
+  // CTAs for every 8 rows of the largest request, and no more than the device
+  // holds at once; they start while the main kernel ends and wait for it there
+  const long long rows = (long long)P.max_nodes * P.group, warps = (rows + 7) / 8 * P.heads;
+  const long long want = (warps + kJoinWarps - 1) / kJoinWarps;
+  const long long most = (12ll * num_sms + P.B - 1) / P.B;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(P.B, (unsigned)max(1ll, min(want, most)));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D>, P) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  return 0;
+}
+
+template <typename T>
+int launch_join_dim(const TreeParams& P, int num_sms, cudaStream_t s) {
+  switch (P.dim) {
+    case 64: return launch_join<T, 64>(P, num_sms, s);
+    case 96: return launch_join<T, 96>(P, num_sms, s);
+    case 128: return launch_join<T, 128>(P, num_sms, s);
+    case 192: return launch_join<T, 192>(P, num_sms, s);
+    case 256: return launch_join<T, 256>(P, num_sms, s);
+    default: return -1;
+  }
+}
+}  // namespace
+
 int launch_tree_join(const TreeParams& P, bool bf16, int num_sms, cudaStream_t s) {
-  // enough CTAs for every row of the largest request, and no more than the
-  // device holds at once
-  const long long rows = (long long)P.max_nodes * P.heads * P.group;
-  const long long want = (rows + kJoinWarps - 1) / kJoinWarps;
-  const long long most = (8ll * num_sms + P.B - 1) / P.B;
-  const dim3 grid(P.B, (unsigned)max(1ll, min(want, most)));
-  if (bf16)
-    tree_join_kernel<__nv_bfloat16><<<grid, kJoinWarps * 32, 0, s>>>(P);
-  else
-    tree_join_kernel<__half><<<grid, kJoinWarps * 32, 0, s>>>(P);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return bf16 ? launch_join_dim<__nv_bfloat16>(P, num_sms, s) : launch_join_dim<__half>(P, num_sms, s);
 }
 
 }  // namespace sv

@@ -128,9 +128,8 @@ __device__ __forceinline__ int tree_owner(long long x, long long T, int G) {
   return (int)(((x + 1) * G + T - 1) / T - 1);
 }
 
-// A run of tiles of one item inside a CTA's range.
+// A run of tiles of one item inside a CTA's range (of the walk's request).
 struct TreeSeg {
-  TreeReq r;
   int b, kvh, m;   // request, key/value head, row block
   int t0, t1;      // its tiles
 };
@@ -159,7 +158,6 @@ struct TreeWalk {
     }
     const long long off = x - first;
     const int item = (int)(off / r.per_item);
-    g.r = r;
     g.b = b;
     g.t0 = (int)(off - (long long)item * r.per_item);
     g.t1 = (int)min((long long)r.per_item, g.t0 + (end - x));

@@ -31,7 +31,7 @@ struct TreeParams {
   void* out;
   float* lse;      // or null
   int32_t* status; // or null
-  float* part_o;   // [2 * grid][rows][dim] unnormalised outputs of split items
+  float* part_o;   // [2 * grid][dim / 4][rows][4] unnormalised outputs of split items
   float2* part_ml; // [2 * grid][rows] their reference (log2 units) and sum
   int32_t* failed; // [grid] whether a wait of a CTA ran out, or null
   long long* start;  // [B + 1] first tile of each request (main kernel to combine)

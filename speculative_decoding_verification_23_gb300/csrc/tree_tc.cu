@@ -8,7 +8,8 @@
 namespace sv {
 namespace {
 
-constexpr int kTcKeys = 128;     // keys per tile
+constexpr int kTcKeys = 128;     // keys per staged tile
+constexpr int kUnit = 64;        // keys per unit of work, half a tile
 constexpr int kTcRows = 128;     // query rows per tile (lanes of tensor memory)
 constexpr int kNewBox = 16;      // drafted tokens per TMA box
 constexpr float kLazy = 8.f;     // log2: how far a row's maximum may pass its reference
@@ -22,6 +23,9 @@ struct TcShape {
   static constexpr int kSmem = NT * kQBytes + kSlots * kSlot + 1024;  // 1024: alignment
   static constexpr int kWarps = 4 * NT + 2;
   static constexpr int kThreads = 32 * kWarps;
+  // Score buffers per row tile.  With two, scores are issued after the product
+  // two units before: when they arrive, at most one product is not in O.
+  static constexpr int kBufs = 2;
 };
 
 struct TcMaps {
@@ -68,13 +72,27 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 32 columns of this warp's 32 lanes; the wait is part of the load, so that
-// no use of a register can move before it.
+// The wait for tensor-memory loads, and a use of their 32 registers that
+// stands behind it, so that no other use can move before the wait.
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void loaded(float* r) {
+  asm volatile(""
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]),
+                 "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]),
+                 "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]),
+                 "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+                 "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
+                 "+f"(r[30]), "+f"(r[31])
+               :
+               : "memory");
+}
+
+// 32 columns of this warp's 32 lanes; valid after the wait.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-      "%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+      "%30,%31}, [%32];"
       : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
         "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
         "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
@@ -82,15 +100,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* r) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const float* r) {
+// 16 columns, with the wait.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
-      "%31,%32};" ::"r"(addr),
-      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
-      "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]),
-      "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]),
-      "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
@@ -118,6 +135,16 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int c
       : "memory");
 }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
+// A value that all lanes share, in a form the compiler knows to be uniform:
+// the products take their descriptors from uniform registers.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // A bounded wait of a whole warp, with one outcome for all lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
@@ -136,10 +163,12 @@ __device__ __forceinline__ uint32_t tree_bits32(const TreeParams& P, int cu, int
   return left >= 32 ? bits : (left <= 0 ? 0u : bits & ((1u << left) - 1u));
 }
 
-// A tile's keys: [lo, lo + valid) of the cached or of the drafted ones.
+// A tile's keys: [lo, lo + valid) of the cached or of the drafted ones, in
+// one or two units.
 struct TcTile {
   bool cached;
   int lo, valid, n16;
+  __device__ __forceinline__ int unit16(int h) const { return min(kUnit, n16 - h * kUnit); }
 };
 __device__ __forceinline__ TcTile tc_tile(const TreeReq& r, int t) {
   TcTile x;
@@ -150,29 +179,65 @@ __device__ __forceinline__ TcTile tc_tile(const TreeReq& r, int t) {
   return x;
 }
 
+// Adds the infinities and NaN among the drafted values [lo, hi) that a row
+// sees to its result, which was computed with zeros in their places: to the
+// written row `dst`, or to its partial result (unnormalised: the weight's
+// size does not matter).
+template <typename T, int D>
+__device__ __noinline__ void add_odd(const TreeParams& P, int cu, int n, int node, int kvh, int lo, int hi, T* dst,
+                                     float4* part) {
+  const uint32_t em = exp_mask<T>();
+  for (int j = lo; j < hi; ++j) {
+    if (!((tree_bits32(P, cu, n, node, j & ~31) >> (j & 31)) & 1u)) continue;
+    const uint16_t* v = static_cast<const uint16_t*>(P.v_new) + (long long)(cu + j) * P.sn_node + (long long)kvh * P.sn_head;
+    for (int d = 0; d < D; ++d) {
+      const uint32_t b = v[d];
+      if ((b & em) != em) continue;
+      if (dst) {
+        uint16_t* o = reinterpret_cast<uint16_t*>(dst + d);
+        *o = (uint16_t)(pack2<T>(half_to_f32<T>(*o) + half_to_f32<T>(b), 0.f) & 0xffffu);
+      } else {
+        reinterpret_cast<float*>(part + (long long)(d / 4) * P.rows)[d & 3] += half_to_f32<T>(b);
+      }
+    }
+  }
+}
+
+// The units of a segment in order, for one role.
+struct TcCursor {
+  int t, h;
+  __device__ __forceinline__ void next(const TreeReq& r) {
+    if (h == 0 && tc_tile(r, t).n16 > kUnit) {
+      h = 1;
+    } else {
+      ++t;
+      h = 0;
+    }
+  }
+};
+
 // Warps 0 .. 4 NT - 1: one query row a thread (the softmax); then one warp
 // that copies tiles, one whose first lane issues the products.
 //
-// The unit of work is a tile of keys for one of the NT tiles of rows.  Units
-// alternate between two score buffers in tensor memory:
+// A unit is 64 keys of a staged tile, for each of the NT tiles of rows:
 //   S = Q K^T (both from shared memory), softmax by the row's thread, P in
 //   16 bits over S's first columns, O += P V (P from tensor memory).
-// With NT = 2 a buffer belongs to a row tile, and both use a staged tile;
-// with NT = 1 the scores of the next tile are computed during the softmax.
+// A row tile's units alternate between two score buffers, so that the scores
+// ahead are computed while a softmax runs.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     tree_tc_kernel(const TreeParams P, const __grid_constant__ TcMaps maps, int box) {
   using S = TcShape<D, NT>;
   constexpr int HD = D / 64;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t full[S::kSlots], empty[S::kSlots], q_full, s_full[2], p_ready[2], o_done[NT], seg_end, fin;
+  __shared__ uint64_t full[S::kSlots], empty[S::kSlots], q_full, s_full[4], p_ready[4], o_done[NT], o_last[NT], seg_end, fin;
   __shared__ uint32_t tmem_at;
   // the last segments with a bad page (the copies run at most kSlots / 2
   // segments ahead) and with infinities or NaN among the drafted values
   __shared__ volatile int bad_seg[16], odd_seg[2], dead;
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   unsigned char* ring = smem + NT * S::kQBytes;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
 
   if (warp == 4 * NT + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_at))
@@ -185,11 +250,14 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
       mbar_init(&empty[i], 1);
     }
     mbar_init(&q_full, NT * 128);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], 128);
     }
-    for (int i = 0; i < NT; ++i) mbar_init(&o_done[i], 1);
+    for (int i = 0; i < NT; ++i) {
+      mbar_init(&o_done[i], 1);
+      mbar_init(&o_last[i], 1);
+    }
     mbar_init(&seg_end, NT * 128);
     mbar_init(&fin, 1);
     fence_mbar_init();
@@ -197,12 +265,13 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     odd_seg[0] = odd_seg[1] = -1;
     dead = 0;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const TreeScan scan = tree_scan(P, lane);
   if (blockIdx.x == 0 && warp == 0) tree_store_starts(P, scan, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_at;
+  const uint32_t tmem = uniform(tmem_at);
   TreeWalk walk;
   walk.begin(P, lane, scan, blockIdx.x);
   TreeSeg g;
@@ -215,7 +284,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     bool ok = true;
     for (int seg = 0; ok && walk.next(P, g); ++seg) {
       for (int t = g.t0; ok && t < g.t1; ++t, ++tc) {
-        const TcTile x = tc_tile(g.r, t);
+        const TcTile x = tc_tile(walk.r, t);
         const int rows = x.cached ? box : kNewBox, nb = (x.valid + rows - 1) / rows;
         const uint32_t bytes = (uint32_t)(nb * rows * 128 * HD);
         // boxes of a tile by lane (at most 16 boxes of 8 slots, HD halves each)
@@ -251,7 +320,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
               if (x.cached)
                 tma_4d(at, kv ? &maps.v : &maps.k, half * 64, slot[e], g.kvh, page[e], &full[s]);
               else
-                tma_3d(at, kv ? &maps.vn : &maps.kn, half * 64, g.r.cu + x.lo + bx * rows, g.kvh, &full[s]);
+                tma_3d(at, kv ? &maps.vn : &maps.kn, half * 64, walk.r.cu + x.lo + bx * rows, g.kvh, &full[s]);
             }
           }
         }
@@ -264,97 +333,132 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
   } else if (warp == 4 * NT + 1) {
     // ---------------------------------------------------------- products
     bool ok = true;
-    uint32_t p_ph[2] = {0, 0}, q_ph = 0;
+    uint32_t p_ph = 0, q_ph = 0;  // p_ph: a bit per buffer
     const uint32_t q_at = smem_u32(smem), r_at = smem_u32(ring);
+    auto wait_full = [&](int f) { return warp_wait(&full[f % S::kSlots], (f / S::kSlots) & 1); };
     while (ok && walk.next(P, g)) {
-      const int tiles = g.t1 - g.t0, units = tiles * NT;
       ok = warp_wait(&q_full, q_ph);
       q_ph ^= 1;
-      tc_fence_after();
-      auto wait_full = [&](int f) { return warp_wait(&full[f % S::kSlots], (f / S::kSlots) & 1); };
-      auto scores = [&](int u) {
-        const int i = u / NT, w = NT == 1 ? 0 : u & 1, f = 2 * (tc + i), s = f % S::kSlots;
-        if (w == 0) {
-          ok = ok && wait_full(f);
-          tc_fence_after();
-        }
+      // scores of one unit for all row tiles, into buffer n % kBufs of each
+      TcCursor a{g.t0, 0};
+      int an = 0;
+      auto scores = [&](int w) {
+        const int f = 2 * (tc + a.t - g.t0), s = f % S::kSlots;
+        if (a.h == 0 && w == 0) ok = ok && wait_full(f);
+        tc_fence_after();
         if (!ok) return;
-        if (lane == 0) {
-          const TcTile x = tc_tile(g.r, g.t0 + i);
-          const uint32_t id = inst_desc<T>(x.n16, false);
-          const uint32_t a = q_at + w * S::kQBytes, b = r_at + s * S::kSlot;
+        const TcTile x = tc_tile(walk.r, a.t);
+        const int buf = uniform(w * S::kBufs + an % S::kBufs);
+        const uint32_t id = uniform(inst_desc<T>(x.unit16(a.h), false));
+        const uint32_t at = uniform(r_at + s * S::kSlot + a.h * (kUnit * 128));
+        if (elect_one()) {
+          const uint64_t da = smem_desc(q_at + w * S::kQBytes, 16, 1024);
+          const uint64_t db = smem_desc(at, 16, 1024);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (ks / 4) * S::kHalf + (ks % 4) * 32;
-            mma_ss(tmem + (u & 1) * kTcKeys, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), id, ks > 0);
+            const uint32_t off = ((ks / 4) * S::kHalf + (ks % 4) * 32) >> 4;
+            mma_ss(tmem + buf * kUnit, da + off, db + off, id, ks > 0);
           }
-          mma_commit(&s_full[u & 1]);
-          if (w == NT - 1) mma_commit(&empty[s]);
+          mma_commit(&s_full[buf]);
+          if (w == NT - 1 && (a.h == 1 || x.n16 <= kUnit)) mma_commit(&empty[s]);
         }
         __syncwarp();
+        if (w == NT - 1) {
+          a.next(walk.r);
+          ++an;
+        }
       };
-      scores(0);
-      if (units > 1) scores(1);
-      for (int u = 0; ok && u < units; ++u) {
-        const int i = u / NT, w = NT == 1 ? 0 : u & 1, f = 2 * (tc + i) + 1, s = f % S::kSlots;
-        ok = warp_wait(&p_ready[u & 1], p_ph[u & 1]);
-        p_ph[u & 1] ^= 1;
-        if (w == 0) ok = ok && wait_full(f);
-        tc_fence_after();
-        if (!ok) break;
-        if (lane == 0) {
-          const TcTile x = tc_tile(g.r, g.t0 + i);
+      for (int i = 0; i < S::kBufs && a.t < g.t1; ++i)
+#pragma unroll
+        for (int w = 0; w < NT; ++w) scores(w);
+      TcCursor c{g.t0, 0};
+      for (int cn = 0; ok && c.t < g.t1; ++cn) {
+        const int f = 2 * (tc + c.t - g.t0) + 1, s = f % S::kSlots;
+        const TcTile x = tc_tile(walk.r, c.t);
+        const bool last = c.h == 1 || x.n16 <= kUnit, final = last && c.t == g.t1 - 1, more = a.t < g.t1;
+#pragma unroll
+        for (int w = 0; w < NT; ++w) {
+          const int buf = w * S::kBufs + cn % S::kBufs;
+          ok = ok && warp_wait(&p_ready[buf], (p_ph >> buf) & 1);
+          p_ph ^= 1u << buf;
+          if (w == 0 && c.h == 0) ok = ok && wait_full(f);
+          tc_fence_after();
+          if (!ok) break;
           const uint32_t id = inst_desc<T>(D, true);
-          const uint32_t o = tmem + 2 * kTcKeys + w * D, p = tmem + (u & 1) * kTcKeys, v = r_at + s * S::kSlot;
-          for (int ks = 0; ks < x.n16 / 16; ++ks)
-            mma_ts(o, p + ks * 8, smem_desc(v + ks * 2048, S::kHalf, 1024), id, i > 0 || ks > 0);
-          mma_commit(&o_done[w]);
-          if (w == NT - 1) mma_commit(&empty[s]);
+          const uint32_t o = tmem + 4 * kUnit + w * D, p = uniform(tmem + buf * kUnit);
+          const uint32_t at = uniform(r_at + s * S::kSlot + c.h * (kUnit * 128));
+          const int steps = uniform(x.unit16(c.h) / 16);
+          if (elect_one()) {
+            const uint64_t dv = smem_desc(at, S::kHalf, 1024);
+#pragma unroll
+            for (int ks = 0; ks < kUnit / 16; ++ks)
+              if (ks < steps) mma_ts(o, p + ks * 8, dv + ks * (2048 >> 4), id, cn > 0 || ks > 0);
+            mma_commit(&o_done[w]);
+            if (final) mma_commit(&o_last[w]);
+            if (w == NT - 1 && last) mma_commit(&empty[s]);
+          }
+          __syncwarp();
+          if (more) scores(w);
         }
-        __syncwarp();
-        if (u + 2 < units) scores(u + 2);
+        c.next(walk.r);
       }
-      tc += tiles;
+      tc += g.t1 - g.t0;
     }
     if (!ok) dead = 1;
-    if (lane == 0) mma_commit(&fin);
+    if (elect_one()) mma_commit(&fin);
     __syncwarp();
     mbar_wait(&fin, 0);  // every product has ended before tensor memory is freed
-  } else {
+  } else if (warp < 4 * NT) {
     // ----------------------------------------------------------- softmax
     const int w = warp >> 2, row = (warp & 3) * 32 + lane, wtid = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t o_at = tmem + lanes + 2 * kTcKeys + w * D;
+    const uint32_t o_at = tmem + lanes + 4 * kUnit + w * D;
     unsigned char* qs = smem + w * S::kQBytes;
-    uint32_t s_ph[2] = {0, 0};
+    uint32_t s_ph = 0;  // a bit per buffer
+    // node of a row: exact, as rows are below 2^22 and half a row from a multiple
+    const float inv_group = 1.f / (float)P.group;
     uint32_t o_n = 0;  // products on this tile's output so far
     bool ok = true;
     for (int seg = 0; ok && walk.next(P, g); ++seg) {
-      const TreeReq& r = g.r;
+      const TreeReq& r = walk.r;
       const int row_lo = g.m * (NT * kTcRows) + w * kTcRows;
       const int nrows = min(kTcRows, r.n * P.group - row_lo);  // may be <= 0
-      // this tile's query rows, swizzled as TMA would: 8 rows of 128 bytes a pattern
-      for (int i = wtid; i < kTcRows * (D / 8); i += 128) {
-        const int rr = i / (D / 8), ch = i % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (rr < nrows) {
-          const int R = row_lo + rr;
-          v = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + (long long)(r.cu + R / P.group) * P.sq_node +
-                                              (long long)(g.kvh * P.group + R % P.group) * P.sq_head + ch * 8);
+      // This tile's query rows, swizzled as TMA would: 8 rows of 128 bytes a
+      // pattern.  A thread copies one 16-byte piece of every (1024 / D)-th
+      // row, with 8 loads in flight.
+      constexpr int STEP = 1024 / D, N = 8;
+      const int ch = wtid % (D / 8);
+      const T* src = static_cast<const T*>(P.q) + (long long)r.cu * P.sq_node + ch * 8;
+#pragma unroll 1
+      for (int r0 = wtid / (D / 8); r0 < kTcRows; r0 += N * STEP) {
+        uint4 v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int rr = r0 + i * STEP, R = row_lo + rr;
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (rr < nrows) {
+            const int nd = (int)(((float)R + 0.5f) * inv_group);
+            v[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)nd * P.sq_node +
+                                                        (long long)(g.kvh * P.group + R - nd * P.group) * P.sq_head));
+          }
         }
-        *reinterpret_cast<uint4*>(qs + (ch >> 3) * (kTcRows * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int rr = r0 + i * STEP;
+          *reinterpret_cast<uint4*>(qs + (ch >> 3) * (kTcRows * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v[i];
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(&q_full);
       const bool mine = row < nrows;
       const bool any = (warp & 3) * 32 < nrows;  // warp-uniform
       const int R = row_lo + (mine ? row : 0);
-      const int node = mine ? R / P.group : 0;
+      const int node = mine ? (int)(((float)R + 0.5f) * inv_group) : 0;
       float m = -INFINITY;                 // the row's reference, log2 units
-      float2 l2 = make_float2(0.f, 0.f);   // its sum of 2^(s - m)
+      float2 l2 = make_float2(0.f, 0.f), l3 = l2;  // its sum of 2^(s - m)
+      int un = 0;                          // units of this segment so far
       for (int t = g.t0; ok && t < g.t1; ++t, ++tc) {
         const TcTile x = tc_tile(r, t);
-        const int buf = NT == 1 ? (t - g.t0) & 1 : w;
         uint32_t see[4];
         if (!x.cached && any) {
 #pragma unroll
@@ -398,89 +502,97 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
           if (odd) odd_seg[seg & 1] = seg;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        ok = ok && warp_wait(&s_full[buf], s_ph[buf]);
-        s_ph[buf] ^= 1;
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t s_at = tmem + lanes + buf * kTcKeys;
-        if (any) {
-          // 32 scores of this row, -inf where it sees nothing; read twice (for
-          // the maximum, for the weights) to keep registers for one warp more
-          auto chunk = [&](int c, float* z) {
-            tmem_ld32(s_at + c * 32, z);
-            if (x.valid < kTcKeys || !x.cached) {
-              const int left = x.valid - c * 32;
-              const uint32_t bits = x.cached ? (left >= 32 ? 0xffffffffu : (1u << left) - 1u) : see[c];
+#pragma unroll 1
+        for (int h = 0; ok && h * kUnit < x.n16; ++h, ++un) {
+          const int buf = w * S::kBufs + un % S::kBufs;
+          ok = warp_wait(&s_full[buf], (s_ph >> buf) & 1);
+          s_ph ^= 1u << buf;
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t s_at = tmem + lanes + buf * kUnit;
+          if (any) {
+            float z[kUnit];
+            tmem_ld32(s_at, z);
+            tmem_ld32(s_at + 32, z + 32);
+            tmem_wait_ld();
+            loaded(z);
+            loaded(z + 32);
+            if (x.valid < kTcKeys || !x.cached) {  // -inf where the row sees nothing
 #pragma unroll
-              for (int e = 0; e < 32; ++e) z[e] = (bits >> e) & 1u ? z[e] : -INFINITY;
-            }
-          };
-          float mx = -INFINITY;
+              for (int c = 0; c < 2; ++c) {
+                const int left = x.valid - h * kUnit - c * 32;
+                const uint32_t old = left >= 32 ? 0xffffffffu : (left <= 0 ? 0u : (1u << left) - 1u);
+                const uint32_t bits = x.cached ? old : (h == 0 ? see[c] : see[2 + c]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c * 32 >= x.valid) break;
-            float z[32];
-            chunk(c, z);
-            float a = fmaxf(z[0], z[1]), b = fmaxf(z[2], z[3]);
-#pragma unroll
-            for (int e = 4; e < 32; e += 4) {
-              a = fmaxf(a, fmaxf(z[e], z[e + 1]));
-              b = fmaxf(b, fmaxf(z[e + 2], z[e + 3]));
-            }
-            mx = fmaxf(mx, fmaxf(a, b));
-          }
-          mx *= P.scale_log2;  // the scale is positive
-          // The reference follows the maximum only where it falls more than
-          // 2^8 behind (or has none yet): weights up to 2^8 are exact in
-          // fp32 sums and in range of both 16-bit types.
-          const bool move = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
-          if (__any_sync(0xffffffffu, move)) {
-            const float f = move ? (m == -INFINITY ? 0.f : ex2(m - mx)) : 1.f;
-            if (move) {
-              m = mx;
-              l2.x *= f;
-              l2.y *= f;
-            }
-            if (t > g.t0) {
-              ok = warp_wait(&o_done[w], (o_n - 1) & 1);  // the tile before is in O
-              if (!ok) break;
-              __syncwarp();
-              tc_fence_after();
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                tmem_ld32(o_at + c * 32, o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= f;
-                tmem_st32(o_at + c * 32, o);
+                for (int e = 0; e < 32; ++e) z[c * 32 + e] = (bits >> e) & 1u ? z[c * 32 + e] : -INFINITY;
               }
             }
-          }
-          const float ref = m == -INFINITY ? 0.f : m;
-          const float2 sc = make_float2(P.scale_log2, P.scale_log2), nr = make_float2(-ref, -ref);
+            float top[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c * 32 >= x.valid) break;
-            float z[32];
-            uint32_t p[16];
-            chunk(c, z);
+            for (int k = 0; k < 4; ++k) top[k] = fmaxf(z[2 * k], z[2 * k + 1]);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 y = __ffma2_rn(make_float2(z[e], z[e + 1]), sc, nr);
-              const float2 w2 = make_float2(ex2(y.x), ex2(y.y));
-              l2 = __fadd2_rn(l2, w2);
-              p[e / 2] = pack2<T>(w2.x, w2.y);
+            for (int e = 8; e < kUnit; e += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], z[e + 2 * k]), z[e + 2 * k + 1]);
+            // the scale is positive
+            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * P.scale_log2;
+            // The reference follows the maximum only where it falls more than
+            // 2^8 behind (or has none yet): weights up to 2^8 are exact in
+            // fp32 sums and in range of both 16-bit types.
+            const bool move = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
+            if (__any_sync(0xffffffffu, move)) {
+              const float f = move ? (m == -INFINITY ? 0.f : ex2(m - mx)) : 1.f;
+              if (move) {
+                m = mx;
+                l2.x *= f;
+                l2.y *= f;
+                l3.x *= f;
+                l3.y *= f;
+              }
+              if (un > 0) {
+                ok = warp_wait(&o_done[w], (o_n - 1) & 1);  // the unit before is in O
+                if (!ok) break;
+                __syncwarp();
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {  // 16 at a time, beside the 64 scores
+                  uint32_t o[16];
+                  tmem_ld16(o_at + c * 16, o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st16(o_at + c * 16, o);
+                }
+              }
             }
-            tmem_st16(s_at + c * 16, p);  // over scores that have been read
+            const float ref = m == -INFINITY ? 0.f : m;
+            const float2 sc = make_float2(P.scale_log2, P.scale_log2), nr = make_float2(-ref, -ref);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t p[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float* y = z + c * 32 + e;
+                const float2 a = __ffma2_rn(make_float2(y[0], y[1]), sc, nr);
+                const float2 b = __ffma2_rn(make_float2(y[2], y[3]), sc, nr);
+                const float2 ea = make_float2(ex2(a.x), ex2(a.y)), eb = make_float2(ex2(b.x), ex2(b.y));
+                l2 = __fadd2_rn(l2, ea);
+                l3 = __fadd2_rn(l3, eb);
+                p[e / 2] = pack2<T>(ea.x, ea.y);
+                p[e / 2 + 1] = pack2<T>(eb.x, eb.y);
+              }
+              tmem_st16(s_at + c * 16, p);
+            }
+            tc_wait_st();
           }
-          tc_wait_st();
+          ++o_n;
+          tc_fence_before();
+          mbar_arrive(&p_ready[buf]);
         }
-        ++o_n;
-        tc_fence_before();
-        mbar_arrive(&p_ready[buf]);
       }
       if (!ok) break;
-      ok = warp_wait(&o_done[w], (o_n - 1) & 1);
+      // o_done may be one or two products behind here, which its parity does
+      // not tell: the segment's last product has a barrier of its own
+      ok = warp_wait(&o_last[w], seg & 1);
       if (!ok) break;
       tc_fence_after();
       if (NT > 1) {  // odd_seg is written by the first row tile's threads
@@ -492,30 +604,20 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
       const bool poison = bad_seg[seg & 15] == seg, odd = odd_seg[seg & 1] == seg;
       const bool whole = g.t0 == 0 && g.t1 == r.per_item;
       const int slot = 2 * blockIdx.x + tree_slot(g.t0 == 0);
-      float l = l2.x + l2.y;
+      float l = (l2.x + l2.y) + (l3.x + l3.y);
       if (poison) l = NAN;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int head = g.kvh * P.group + R % P.group;
+      const int head = g.kvh * P.group + R - node * P.group;
       T* dst = static_cast<T*>(P.out) + (long long)(r.cu + node) * P.so_node + (long long)head * P.so_head;
       const long long prow = (long long)slot * P.rows + w * kTcRows + row;
-      float* part = P.part_o + prow * D;
+      float4* part = reinterpret_cast<float4*>(P.part_o) + (long long)slot * P.rows * (D / 4) + w * kTcRows + row;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         float o[32];
         __syncwarp();
         tmem_ld32(o_at + c * 32, o);
-        if (mine && odd) {
-          const T* vn = static_cast<const T*>(P.v_new) + (long long)r.cu * P.sn_node + (long long)g.kvh * P.sn_head + c * 32;
-          const int lo = max(0, g.t0 - r.ct) * kTcKeys, hi = min(r.n, (g.t1 - r.ct) * kTcKeys);
-          for (int j = lo; j < hi; ++j) {
-            if (!((tree_bits32(P, r.cu, r.n, node, j & ~31) >> (j & 31)) & 1u)) continue;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const uint32_t b = *reinterpret_cast<const uint16_t*>(vn + (long long)j * P.sn_node + e);
-              if ((b & exp_mask<T>()) == exp_mask<T>()) o[e] += half_to_f32<T>(b);
-            }
-          }
-        }
+        tmem_wait_ld();
+        loaded(o);
         if (mine && whole) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
@@ -529,10 +631,13 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
         } else if (mine) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(part + c * 32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            part[(c * 8 + e / 4) * P.rows] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       if (mine) {
+        if (odd)
+          add_odd<T, D>(P, walk.r.cu, walk.r.n, node, g.kvh, max(0, g.t0 - walk.r.ct) * kTcKeys,
+                        min(walk.r.n, (g.t1 - walk.r.ct) * kTcKeys), whole ? dst : nullptr, part);
         const float ref = m == -INFINITY ? 0.f : m;
         if (!whole)
           P.part_ml[prow] = make_float2(m, l);
