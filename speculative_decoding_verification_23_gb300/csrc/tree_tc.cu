@@ -9,7 +9,7 @@ namespace sv {
 namespace {
 
 constexpr int kTcKeys = 128;     // keys per staged tile
-constexpr int kUnit = 64;        // keys per unit of work, half a tile
+constexpr int kUnit = 64;        // keys per unit of the softmax, half a tile
 constexpr int kTcRows = 128;     // query rows per tile (lanes of tensor memory)
 constexpr int kNewBox = 16;      // drafted tokens per TMA box
 constexpr float kLazy = 8.f;     // log2: how far a row's maximum may pass its reference
@@ -21,11 +21,8 @@ struct TcShape {
   static constexpr int kHalf = kTcKeys * 128;           // 64 channels of a tile
   static constexpr int kSlots = D == 64 ? 10 : (NT == 1 ? 6 : 5);
   static constexpr int kSmem = NT * kQBytes + kSlots * kSlot + 1024;  // 1024: alignment
-  static constexpr int kWarps = 4 * NT + 2;
+  static constexpr int kWarps = 4 * NT + 1 + NT;
   static constexpr int kThreads = 32 * kWarps;
-  // Score buffers per row tile.  With two, scores are issued after the product
-  // two units before: when they arrive, at most one product is not in O.
-  static constexpr int kBufs = 2;
 };
 
 struct TcMaps {
@@ -52,21 +49,28 @@ __device__ __forceinline__ uint32_t inst_desc<__half>(int n, bool vmajor) {
   return (1u << 4) | ((vmajor ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// Issued by the lane with `one`; the whole warp comes here, so that the
+// operands stay in uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc, uint32_t one) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc, uint32_t one) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(smem_u32(bar)),
+      "r"(one)
+      : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -136,10 +140,10 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int c
 }
 
 // One lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t p;
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
-  return p != 0;
+  return p;
 }
 // A value that all lanes share, in a form the compiler knows to be uniform:
 // the products take their descriptors from uniform registers.
@@ -203,34 +207,25 @@ __device__ __noinline__ void add_odd(const TreeParams& P, int cu, int n, int nod
   }
 }
 
-// The units of a segment in order, for one role.
-struct TcCursor {
-  int t, h;
-  __device__ __forceinline__ void next(const TreeReq& r) {
-    if (h == 0 && tc_tile(r, t).n16 > kUnit) {
-      h = 1;
-    } else {
-      ++t;
-      h = 0;
-    }
-  }
-};
-
 // Warps 0 .. 4 NT - 1: one query row a thread (the softmax); then one warp
-// that copies tiles, one whose first lane issues the products.
+// that copies tiles, and for each row tile one that issues its products.
 //
-// A unit is 64 keys of a staged tile, for each of the NT tiles of rows:
-//   S = Q K^T (both from shared memory), softmax by the row's thread, P in
-//   16 bits over S's first columns, O += P V (P from tensor memory).
-// A row tile's units alternate between two score buffers, so that the scores
-// ahead are computed while a softmax runs.
+// For every staged tile and each of the NT tiles of rows:
+//   S = Q K^T (both from shared memory), 128 keys in one go; then by 64 keys
+//   the softmax by the row's thread, P in 16 bits over the scores read, and
+//   O += P V (P from tensor memory), so that the product of one half runs
+//   during the softmax of the other.
+// With NT = 2 the two row tiles share a staged tile, and one's products run
+// during the other's softmax; with NT = 1 there are two score buffers, and
+// the next tile's scores are computed ahead.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     tree_tc_kernel(const TreeParams P, const __grid_constant__ TcMaps maps, int box) {
   using S = TcShape<D, NT>;
   constexpr int HD = D / 64;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t full[S::kSlots], empty[S::kSlots], q_full, s_full[4], p_ready[4], o_done[NT], o_last[NT], seg_end, fin;
+  __shared__ uint64_t full[S::kSlots], empty[S::kSlots], q_full[NT], s_full[2], p_ready[4], o_half[NT], o_done[NT],
+      o_last[NT], fin[NT], seg_end;
   __shared__ uint32_t tmem_at;
   // the last segments with a bad page (the copies run at most kSlots / 2
   // segments ahead) and with infinities or NaN among the drafted values
@@ -247,19 +242,18 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], NT);
     }
-    mbar_init(&q_full, NT * 128);
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_ready[i], 128);
-    }
+    for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&p_ready[i], 128);
     for (int i = 0; i < NT; ++i) {
+      mbar_init(&q_full[i], 128);
+      mbar_init(&o_half[i], 1);
+      mbar_init(&fin[i], 1);
       mbar_init(&o_done[i], 1);
       mbar_init(&o_last[i], 1);
     }
     mbar_init(&seg_end, NT * 128);
-    mbar_init(&fin, 1);
     fence_mbar_init();
     for (int i = 0; i < 16; ++i) bad_seg[i] = -1;
     odd_seg[0] = odd_seg[1] = -1;
@@ -330,94 +324,104 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
       dead = 1;
       fills.drain(full, S::kSlots);
     }
-  } else if (warp == 4 * NT + 1) {
+  } else if (warp > 4 * NT) {
     // ---------------------------------------------------------- products
+    // One warp issues everything of row tile w.  It has little time for a
+    // unit of 64 keys, so slots and phases are counted, not computed, and what
+    // descriptors depend on is uniform.
+    const int w = warp - (4 * NT + 1);
+    const uint32_t one = elect_one();
     bool ok = true;
-    uint32_t p_ph = 0, q_ph = 0;  // p_ph: a bit per buffer
-    const uint32_t q_at = smem_u32(smem), r_at = smem_u32(ring);
-    auto wait_full = [&](int f) { return warp_wait(&full[f % S::kSlots], (f / S::kSlots) & 1); };
+    uint32_t p_ph = 0, q_ph = 0;           // phases (p_ph: a bit per unit buffer)
+    int ks_ = 0, vs_ = 1;                  // next slots of keys and of values
+    uint32_t k_ph = 0, v_ph = 0;           // and their phases
+    const uint64_t da = smem_desc(smem_u32(smem) + w * S::kQBytes, 16, 1024);
+    const uint64_t dk = smem_desc(smem_u32(ring), 16, 1024), dv = smem_desc(smem_u32(ring), S::kHalf, 1024);
+    const uint32_t o = tmem + 2 * kTcKeys + w * D, id_v = inst_desc<T>(D, true);
     while (ok && walk.next(P, g)) {
-      ok = warp_wait(&q_full, q_ph);
+      const int t0 = uniform(g.t0), t1 = uniform(g.t1);
+      TreeReq r;
+      r.ct = uniform(walk.r.ct);
+      r.ctx = uniform(walk.r.ctx);
+      r.n = uniform(walk.r.n);
+      ok = warp_wait(&q_full[w], q_ph);
       q_ph ^= 1;
-      // scores of one unit for all row tiles, into buffer n % kBufs of each
-      TcCursor a{g.t0, 0};
-      int an = 0;
-      auto scores = [&](int w) {
-        const int f = 2 * (tc + a.t - g.t0), s = f % S::kSlots;
-        if (a.h == 0 && w == 0) ok = ok && wait_full(f);
-        tc_fence_after();
+      // scores of tile t
+      auto scores = [&](int t) {
+        const int buf = NT == 1 ? (t - t0) & 1 : w;
+        const uint32_t id = inst_desc<T>(tc_tile(r, t).n16, false);
+        const uint64_t db = dk + (uint32_t)(ks_ * (S::kSlot >> 4));
+        ok = ok && warp_wait(&full[ks_], k_ph);
         if (!ok) return;
-        const TcTile x = tc_tile(walk.r, a.t);
-        const int buf = uniform(w * S::kBufs + an % S::kBufs);
-        const uint32_t id = uniform(inst_desc<T>(x.unit16(a.h), false));
-        const uint32_t at = uniform(r_at + s * S::kSlot + a.h * (kUnit * 128));
-        if (elect_one()) {
-          const uint64_t da = smem_desc(q_at + w * S::kQBytes, 16, 1024);
-          const uint64_t db = smem_desc(at, 16, 1024);
+        tc_fence_after();
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks / 4) * S::kHalf + (ks % 4) * 32) >> 4;
-            mma_ss(tmem + buf * kUnit, da + off, db + off, id, ks > 0);
-          }
-          mma_commit(&s_full[buf]);
-          if (w == NT - 1 && (a.h == 1 || x.n16 <= kUnit)) mma_commit(&empty[s]);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = ((ks / 4) * S::kHalf + (ks % 4) * 32) >> 4;
+          mma_ss(tmem + buf * kTcKeys, da + off, db + off, id, ks > 0, one);
         }
-        __syncwarp();
-        if (w == NT - 1) {
-          a.next(walk.r);
-          ++an;
+        mma_commit(&s_full[buf], one);
+        mma_commit(&empty[ks_], one);
+        ks_ += 2;
+        if (ks_ >= S::kSlots) {
+          ks_ -= S::kSlots;
+          k_ph ^= 1;
         }
       };
-      for (int i = 0; i < S::kBufs && a.t < g.t1; ++i)
+      constexpr int AHEAD = 3 - NT;  // tiles whose scores are issued before the first product
+      scores(t0);
+      if (AHEAD > 1 && t0 + 1 < t1) scores(t0 + 1);
+      for (int t = t0; ok && t < t1; ++t) {
+        const int n16 = tc_tile(r, t).n16, buf = NT == 1 ? (t - t0) & 1 : w;
+        const uint64_t db = dv + (uint32_t)(vs_ * (S::kSlot >> 4));
+        const uint32_t p = tmem + buf * kTcKeys;
+        ok = warp_wait(&full[vs_], v_ph) && warp_wait(&p_ready[buf * 2], (p_ph >> (buf * 2)) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (n16 >= kUnit) {
 #pragma unroll
-        for (int w = 0; w < NT; ++w) scores(w);
-      TcCursor c{g.t0, 0};
-      for (int cn = 0; ok && c.t < g.t1; ++cn) {
-        const int f = 2 * (tc + c.t - g.t0) + 1, s = f % S::kSlots;
-        const TcTile x = tc_tile(walk.r, c.t);
-        const bool last = c.h == 1 || x.n16 <= kUnit, final = last && c.t == g.t1 - 1, more = a.t < g.t1;
-#pragma unroll
-        for (int w = 0; w < NT; ++w) {
-          const int buf = w * S::kBufs + cn % S::kBufs;
-          ok = ok && warp_wait(&p_ready[buf], (p_ph >> buf) & 1);
-          p_ph ^= 1u << buf;
-          if (w == 0 && c.h == 0) ok = ok && wait_full(f);
-          tc_fence_after();
-          if (!ok) break;
-          const uint32_t id = inst_desc<T>(D, true);
-          const uint32_t o = tmem + 4 * kUnit + w * D, p = uniform(tmem + buf * kUnit);
-          const uint32_t at = uniform(r_at + s * S::kSlot + c.h * (kUnit * 128));
-          const int steps = uniform(x.unit16(c.h) / 16);
-          if (elect_one()) {
-            const uint64_t dv = smem_desc(at, S::kHalf, 1024);
-#pragma unroll
-            for (int ks = 0; ks < kUnit / 16; ++ks)
-              if (ks < steps) mma_ts(o, p + ks * 8, dv + ks * (2048 >> 4), id, cn > 0 || ks > 0);
-            mma_commit(&o_done[w]);
-            if (final) mma_commit(&o_last[w]);
-            if (w == NT - 1 && last) mma_commit(&empty[s]);
-          }
-          __syncwarp();
-          if (more) scores(w);
+          for (int ks = 0; ks < kUnit / 16; ++ks)
+            mma_ts(o, p + ks * 8, db + ks * (2048 >> 4), id_v, ks > 0 || t > t0, one);
+        } else {
+          for (int ks = 0; ks < n16 / 16; ++ks) mma_ts(o, p + ks * 8, db + ks * (2048 >> 4), id_v, ks > 0 || t > t0, one);
         }
-        c.next(walk.r);
+        mma_commit(&o_half[w], one);
+        p_ph ^= 1u << (buf * 2);
+        if (n16 > kUnit) {
+          ok = warp_wait(&p_ready[buf * 2 + 1], (p_ph >> (buf * 2 + 1)) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (n16 == kTcKeys) {
+#pragma unroll
+            for (int ks = 4; ks < 8; ++ks) mma_ts(o, p + 32 + ks * 8, db + ks * (2048 >> 4), id_v, true, one);
+          } else {
+            for (int ks = 4; ks < n16 / 16; ++ks) mma_ts(o, p + 32 + ks * 8, db + ks * (2048 >> 4), id_v, true, one);
+          }
+          p_ph ^= 2u << (buf * 2);
+        }
+        mma_commit(&o_done[w], one);  // before the scores that the softmax takes for a sign of it
+        mma_commit(&empty[vs_], one);
+        if (t + AHEAD < t1) scores(t + AHEAD);
+        if (t == t1 - 1) mma_commit(&o_last[w], one);
+        vs_ += 2;
+        if (vs_ >= S::kSlots) {
+          vs_ -= S::kSlots;
+          v_ph ^= 1;
+        }
       }
-      tc += g.t1 - g.t0;
     }
     if (!ok) dead = 1;
-    if (elect_one()) mma_commit(&fin);
+    mma_commit(&fin[w], one);
     __syncwarp();
-    mbar_wait(&fin, 0);  // every product has ended before tensor memory is freed
+    mbar_wait(&fin[w], 0);  // every product has ended before tensor memory is freed
   } else if (warp < 4 * NT) {
     // ----------------------------------------------------------- softmax
     const int w = warp >> 2, row = (warp & 3) * 32 + lane, wtid = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t o_at = tmem + lanes + 4 * kUnit + w * D;
+    const uint32_t o_at = tmem + lanes + 2 * kTcKeys + w * D;
     unsigned char* qs = smem + w * S::kQBytes;
     uint32_t s_ph = 0;  // a bit per buffer
     // node of a row: exact, as rows are below 2^22 and half a row from a multiple
     const float inv_group = 1.f / (float)P.group;
-    uint32_t o_n = 0;  // products on this tile's output so far
     bool ok = true;
     for (int seg = 0; ok && walk.next(P, g); ++seg) {
       const TreeReq& r = walk.r;
@@ -449,14 +453,13 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(&q_full);
+      mbar_arrive(&q_full[w]);
       const bool mine = row < nrows;
       const bool any = (warp & 3) * 32 < nrows;  // warp-uniform
       const int R = row_lo + (mine ? row : 0);
       const int node = mine ? (int)(((float)R + 0.5f) * inv_group) : 0;
       float m = -INFINITY;                 // the row's reference, log2 units
       float2 l2 = make_float2(0.f, 0.f), l3 = l2;  // its sum of 2^(s - m)
-      int un = 0;                          // units of this segment so far
       for (int t = g.t0; ok && t < g.t1; ++t, ++tc) {
         const TcTile x = tc_tile(r, t);
         uint32_t see[4];
@@ -467,7 +470,9 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
         // Values past the end of a tile's keys, whatever the slots hold, are
         // zero for the product, and so are infinities and NaN among drafted
         // values: a row that does not see them would get 0 times them.
-        if (w == 0 && ((x.valid & 15) || !x.cached)) {
+        // Both row tiles' threads see to it before their own weights are ready,
+        // writing the same zeros.
+        if ((x.valid & 15) || !x.cached) {
           const int f = 2 * tc + 1, s = f % S::kSlots;
           ok = warp_wait(&full[s], (f / S::kSlots) & 1);
           unsigned char* vs = ring + s * S::kSlot;
@@ -502,14 +507,14 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
           if (odd) odd_seg[seg & 1] = seg;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
+        const int buf = NT == 1 ? (t - g.t0) & 1 : w;
+        ok = ok && warp_wait(&s_full[buf], (s_ph >> buf) & 1);
+        s_ph ^= 1u << buf;
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll 1
-        for (int h = 0; ok && h * kUnit < x.n16; ++h, ++un) {
-          const int buf = w * S::kBufs + un % S::kBufs;
-          ok = warp_wait(&s_full[buf], (s_ph >> buf) & 1);
-          s_ph ^= 1u << buf;
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t s_at = tmem + lanes + buf * kUnit;
+        for (int h = 0; h * kUnit < x.n16; ++h) {
+          const uint32_t s_at = tmem + lanes + buf * kTcKeys + h * kUnit;
           if (any) {
             float z[kUnit];
             tmem_ld32(s_at, z);
@@ -549,8 +554,13 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                 l3.x *= f;
                 l3.y *= f;
               }
-              if (un > 0) {
-                ok = warp_wait(&o_done[w], (o_n - 1) & 1);  // the unit before is in O
+              if (t > g.t0 || h > 0) {
+                // The unit before is in O.  The scores of this tile came after
+                // the products of the tile two before (or one), so each of
+                // these barriers is at most one phase behind, which is all
+                // that a parity tells.
+                if (tc > 0) ok = warp_wait(&o_done[w], (tc - 1) & 1);
+                if (h > 0) ok = ok && warp_wait(&o_half[w], tc & 1);
                 if (!ok) break;
                 __syncwarp();
                 tc_fence_after();
@@ -584,14 +594,13 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
             }
             tc_wait_st();
           }
-          ++o_n;
           tc_fence_before();
-          mbar_arrive(&p_ready[buf]);
+          mbar_arrive(&p_ready[buf * 2 + h]);
         }
       }
       if (!ok) break;
-      // o_done may be one or two products behind here, which its parity does
-      // not tell: the segment's last product has a barrier of its own
+      // o_done may be two phases behind here: the segment's last product has a
+      // barrier of its own
       ok = warp_wait(&o_last[w], seg & 1);
       if (!ok) break;
       tc_fence_after();
