@@ -8,13 +8,28 @@ namespace {
 
 constexpr int kBmThreads = 256;
 constexpr int kBmWarps = kBmThreads / 32;
-constexpr int kBmUnroll = 4;   // 16-byte loads in flight per lane
-constexpr int kBmCap = 512;    // candidates a warp holds at most
+constexpr int kBmUnroll = 4;      // 16-byte loads of a lane in a chunk
+constexpr int kBmCtas = 3;        // per SM
+constexpr int kBmCap = 2048;      // candidates of a request in shared memory
+constexpr int kBmHot = 1024;      // chunks that may hold candidates
+constexpr int kBeamRows = 2048;   // rows up to which those that are read are counted
+
+// A chunk is what a warp reads at once (1024 bf16 or 512 fp32 logits); a step
+// of a CTA is a chunk for each warp.
+template <typename T>
+struct BmShape {
+  static constexpr int N = Vec<T>::N;
+  static constexpr int kChunk = 32 * N * kBmUnroll;
+  static constexpr int kStep = kBmWarps * kChunk;
+};
 
 // Unsigned order of a float's value (no NaN; -0 as 0).
 __device__ __forceinline__ uint32_t float_key(float z) {
   const uint32_t u = __float_as_uint(z == 0.f ? 0.f : z);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_float(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 __device__ __forceinline__ unsigned long long double_key(double z) {
   const unsigned long long u = (unsigned long long)__double_as_longlong(z == 0.0 ? 0.0 : z);
@@ -24,304 +39,395 @@ __device__ __forceinline__ double key_double(unsigned long long k) {
   return __longlong_as_double((long long)((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
 }
 
-// A warp's candidates: the tokens seen so far that may be among the best K
-// of its part, in shared memory.  Every token that beats (tz, tt) — a larger
-// logit, or the same one at a lower token — is added; K of those seen beat
-// or equal it.
-struct WarpCands {
-  float* z;
-  int* tok;
-  int cnt;
-  float tz;
-  int tt;
-};
+// 2^d for a whole d <= 0 (0 below fp32's normal range).
+__device__ __forceinline__ float pow2_int(float d) { return d > -127.f ? __int_as_float(((int)d + 127) << 23) : 0.f; }
 
-// Keeps the best K of the warp's candidates (its count is above K) and makes
-// the K-th best the new bound.  A bisection over the order keys, by counts of
-// the whole warp, finds the K-th logit; a second one over tokens decides
-// among its equals.
-struct Bound {
-  int cnt;
-  float tz;
-  int tt;
-};
-
-__device__ __noinline__ Bound prune_list(float* cz, int* ct, int cnt, int K, int lane) {
-  constexpr int PER = kBmCap / 32;
-  uint32_t key[PER];
-  int tok[PER];
-  __syncwarp();
+// The largest of kBmUnroll vectors' values (NaN passed over).
+template <typename T>
+__device__ __forceinline__ float max_of(const uint4 (&v)[kBmUnroll]);
+template <>
+__device__ __forceinline__ float max_of<float>(const uint4 (&v)[kBmUnroll]) {
+  float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int at = i * 32 + lane;
-    key[i] = at < cnt ? float_key(cz[at]) : 0u;  // 0: below every finite logit
-    tok[i] = at < cnt ? ct[at] : 0x7fffffff;
+  for (int u = 0; u < kBmUnroll; ++u) {
+    m = fmaxf(fmaxf(m, __uint_as_float(v[u].x)), __uint_as_float(v[u].y));
+    m = fmaxf(fmaxf(m, __uint_as_float(v[u].z)), __uint_as_float(v[u].w));
   }
-  uint32_t t = 0;  // the largest key with at least K at or above it
+  return m;
+}
+template <>
+__device__ __forceinline__ float max_of<__nv_bfloat16>(const uint4 (&v)[kBmUnroll]) {
+  auto pair = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+  __nv_bfloat162 m = __hmax2(pair(v[0].x), pair(v[0].y));
+  m = __hmax2(m, __hmax2(pair(v[0].z), pair(v[0].w)));
+#pragma unroll
+  for (int u = 1; u < kBmUnroll; ++u) {
+    m = __hmax2(m, __hmax2(pair(v[u].x), pair(v[u].y)));
+    m = __hmax2(m, __hmax2(pair(v[u].z), pair(v[u].w)));
+  }
+  const float a = __low2float(m), b = __high2float(m);
+  return fmaxf(fmaxf(a, b), -INFINITY);  // NaN where all are
+}
+
+// A vector at the end of a span: -inf past it.
+template <typename T>
+__device__ __forceinline__ uint4 load_tail(const T* z, int at, int hi) {
+  constexpr int N = Vec<T>::N;
+  const T none = neg_inf<T>();
+  __align__(16) T x[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) x[e] = none;
+  uint4 v = *reinterpret_cast<const uint4*>(x);
+  if (at < hi) {
+    v = __ldg(reinterpret_cast<const uint4*>(z + at));
+    if (at + N > hi) {
+      *reinterpret_cast<uint4*>(x) = v;
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (at + e >= hi) x[e] = none;
+      v = *reinterpret_cast<const uint4*>(x);
+    }
+  }
+  return v;
+}
+
+// A value with at least K of the CTA's 256 values at or above it, and not many
+// more than K where that is quickly found; -inf where fewer are finite.  Any
+// such value does: a bisection over the 32 below the largest, where scores
+// lie as a rule, and over all floats' order where too few do.
+__device__ __forceinline__ float kth_bound(const float* vals, int K, int lane) {
+  float v[kBmThreads / 32];
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kBmThreads / 32; ++i) {
+    v[i] = vals[i * 32 + lane];
+    top = fmaxf(top, v[i]);
+  }
+  top = key_float(__reduce_max_sync(0xffffffffu, float_key(top)));
+  auto count = [&](float x) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kBmThreads / 32; ++i) n += v[i] >= x;
+    return __reduce_add_sync(0xffffffffu, n);
+  };
+  if (!(top > -INFINITY)) return -INFINITY;
+  float lo = top - 32.f, hi = top;
+  int n = count(lo);
+  if (n >= K) {
+#pragma unroll 1
+    for (int i = 0; i < 12 && n > K + K / 2; ++i) {
+      const float mid = 0.5f * (lo + hi);
+      const int m = count(mid);
+      if (m >= K) {
+        lo = mid;
+        n = m;
+      } else {
+        hi = mid;
+      }
+    }
+    return lo;
+  }
+  uint32_t t = 0;
+#pragma unroll 1
   for (int bit = 31; bit >= 0; --bit) {
     const uint32_t probe = t | (1u << bit);
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) n += key[i] >= probe;
-    if (__reduce_add_sync(0xffffffffu, n) >= K) t = probe;
+    const float x = key_float(probe);
+    if (x > -INFINITY && count(x) >= K) t = probe;
+    if (!(x > -INFINITY)) t = probe;  // -inf and below: everything
   }
-  int above = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) above += key[i] > t;
-  const int need = K - __reduce_add_sync(0xffffffffu, above);  // >= 1 of key t
-  int last = 0;  // the largest token of them: fewer than `need` are below it
-  for (int bit = 30; bit >= 0; --bit) {
-    const int probe = last | (1 << bit);
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) n += key[i] == t && tok[i] < probe;
-    if (__reduce_add_sync(0xffffffffu, n) < need) last = probe;
-  }
-  __syncwarp();
-  int at = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const bool keep = key[i] > t || (key[i] == t && tok[i] <= last);
-    const unsigned who = __ballot_sync(0xffffffffu, keep);
-    if (keep) {
-      const int to = at + __popc(who & ((1u << lane) - 1u));
-      cz[to] = __uint_as_float((key[i] & 0x80000000u) ? key[i] & 0x7fffffffu : ~key[i]);
-      ct[to] = tok[i];
-    }
-    at += __popc(who);
-  }
-  __syncwarp();
-  return {at, __uint_as_float((t & 0x80000000u) ? t & 0x7fffffffu : ~t), last};
+  return t > 0u ? key_float(t) : -INFINITY;
 }
 
-__device__ __forceinline__ void prune(WarpCands& c, int K, int lane) {
-  const Bound n = prune_list(c.z, c.tok, c.cnt, K, lane);
-  c.cnt = n.cnt;
-  c.tz = n.tz;
-  c.tt = n.tt;
-}
-
-// Adds a vector's tokens (base + e for this lane) that beat the bound.
-template <int N>
-__device__ __forceinline__ void gather(WarpCands& c, const float (&z)[N], int base, int K, int lane) {
-  if (c.cnt + 32 * N > kBmCap) prune(c, K, lane);  // cnt > K here: K + 32 N <= kBmCap
-#pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const bool in = z[e] > c.tz || (z[e] == c.tz && base + e < c.tt);
-    const unsigned who = __ballot_sync(0xffffffffu, in);
-    if (in) {
-      const int to = c.cnt + __popc(who & ((1u << lane) - 1u));
-      c.z[to] = z[e];
-      c.tok[to] = base + e;
-    }
-    c.cnt += __popc(who);
+// ---- the split of all rows' logits over the CTAs
+// A row that is read (its beam has not ended and is alive) has `steps` steps.
+// All steps of all such rows, in order, are cut evenly over the CTAs; a row's
+// piece in a CTA has a record of its sum, and each of its chunks its maximum.
+// With more than kBeamRows rows, rows that need not be read keep their places
+// in the split and are passed over.
+struct BeamSplit {
+  const int* rows;   // the rows that are read, or null: all
+  int n;             // how many
+  int steps, used;   // steps per row, CTAs in use
+  long long total;
+  bool small;        // (total + 1) * (used + 1) fits 32 bits, whose divisions are much faster
+  __device__ __forceinline__ int row(int a) const { return rows ? rows[a] : a; }
+  __device__ __forceinline__ long long begin(int c) const {
+    return small ? (long long)((uint32_t)total * (uint32_t)c / (uint32_t)used) : total * c / used;
   }
+  __device__ __forceinline__ int owner(long long x) const {
+    return small ? (int)(((uint32_t)(x + 1) * (uint32_t)used + (uint32_t)total - 1u) / (uint32_t)total) - 1
+                 : (int)(((x + 1) * used + total - 1) / total - 1);
+  }
+  __device__ __forceinline__ int first_cta(int a) const { return owner((long long)a * steps); }
+  __device__ __forceinline__ int pieces(int a) const { return owner((long long)(a + 1) * steps - 1) - first_cta(a) + 1; }
+  // the record of place a's piece in a CTA, `per` of which a CTA has
+  __device__ __forceinline__ int record(int cta, int a, int per) const { return cta * per + a - (int)((uint32_t)begin(cta) / (uint32_t)steps); }
+};
+
+__device__ __forceinline__ bool beam_read(const BeamParams& P, int row) {
+  return P.scores[row] > -INFINITY && !(P.finished && P.finished[row] != 0);
 }
 
-// One CTA per (row, span of its vocabulary): one read of the span's logits
-// for the row's sum of exponentials and for its best K tokens.  The last CTA
-// of a request picks its continuations.
+struct BeamShared {
+  float w_ref[kBmWarps], w_sum[kBmWarps], w_top[kBmWarps];
+  int w_cnt[kBmWarps];
+  float t_max[kBmThreads];
+  int is_last, bad, n_got, n_hot, over;
+  int place[kBeamMax];                       // of each row of the request in the split, -1: not read
+  int pieces[kBeamMax];
+  double lse[kBeamMax], row_sum[kBeamMax];
+  float row_ref[kBeamMax], s0[kBeamMax], add[kBeamMax], err[kBeamMax], z_min[kBeamMax];
+  int row_low[kBeamMax];
+  unsigned long long best_key[kBeamMax];     // the best K, in order
+  int best_flat[kBeamMax];
+};
+
+// A row's tokens [lo, hi) in a CTA.
+struct BeamPiece {
+  int a, row, lo, hi;  // place in the split, row
+};
+
+// The loads of a warp's chunk at token x (of this lane) of a piece.
 template <typename T>
-__global__ void __launch_bounds__(kBmThreads) beam_select_kernel(const BeamParams P) {
-  constexpr int N = Vec<T>::N;
-  extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float w_ref[kBmWarps], w_sum[kBmWarps];
-  __shared__ int w_cnt[kBmWarps], w_at[kBmWarps + 1];
-  __shared__ int is_last;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int sp = blockIdx.x % P.spans, row = blockIdx.x / P.spans;
-  const int b = row / P.W, K = P.keep;
-  const float L = 1.4426950408889634f;
-  float* cz = reinterpret_cast<float*>(smem);            // [warps][cap]
-  int* ct = reinterpret_cast<int*>(cz + kBmWarps * kBmCap);
-  const float cum = P.scores[row];
-  const bool ended = P.finished && P.finished[row] != 0;
-  if (!ended && cum > -INFINITY) {
-    const int lo = sp * P.span, hi = min(P.V, lo + P.span);
-    const T* z0 = static_cast<const T*>(P.logits) + (long long)row * P.ld;
-    WarpCands c;
-    c.z = cz + warp * kBmCap;
-    c.tok = ct + warp * kBmCap;
-    c.cnt = 0;
-    c.tz = -INFINITY;
-    c.tt = -1;
-    // sum + low: the sum with its rounding errors, of 2^((z - ref) log2(e)).
-    // The difference comes first: the lowest finite logits, a mask as a rule,
-    // leave fp32's range when they are scaled.
-    float ref = -INFINITY, sum = 0.f, low = 0.f;
-    bool first = true;
-    constexpr int STEP = kBmThreads * N * kBmUnroll;
-    for (int at = lo; at < hi; at += STEP) {
-      uint4 raw[kBmUnroll];
-      int base[kBmUnroll];
+__device__ __forceinline__ void beam_fetch(const BeamParams& P, const BeamPiece& p, int x, uint4 (&v)[kBmUnroll]) {
+  constexpr int N = BmShape<T>::N;
+  const T* z0 = static_cast<const T*>(P.logits) + (long long)p.row * P.ld;
+  if (x + (kBmUnroll - 1) * 32 * N + N <= p.hi) {
 #pragma unroll
-      for (int u = 0; u < kBmUnroll; ++u) {
-        base[u] = at + ((u * kBmWarps + warp) * 32 + lane) * N;
-        if (base[u] < hi) raw[u] = __ldg(reinterpret_cast<const uint4*>(z0 + base[u]));
-      }
-      float z[kBmUnroll][N], mx[kBmUnroll];
+    for (int u = 0; u < kBmUnroll; ++u) v[u] = __ldg(reinterpret_cast<const uint4*>(z0 + x + u * 32 * N));
+  } else {
+#pragma unroll 1
+    for (int u = 0; u < kBmUnroll; ++u) {
+      const uint4 t = load_tail<T>(z0, x + u * 32 * N, p.hi);
 #pragma unroll
-      for (int u = 0; u < kBmUnroll; ++u) {
-        if (base[u] < hi) {
-          cvt16(raw[u], z[u]);
-          if (base[u] + N > hi) {
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-              if (base[u] + e >= hi) z[u][e] = -INFINITY;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < N; ++e) z[u][e] = -INFINITY;
-        }
-        mx[u] = z[u][0];
-#pragma unroll
-        for (int e = 1; e < N; ++e) mx[u] = fmaxf(mx[u], z[u][e]);
-      }
-      float top = mx[0];
-#pragma unroll
-      for (int u = 1; u < kBmUnroll; ++u) top = fmaxf(top, mx[u]);
-      if (first) {
-        // The first vectors' 64 maxima of half a lane's tokens: K tokens are
-        // at or above the K-th of them.
-        float a = mx[0], d = mx[kBmUnroll / 2];
-#pragma unroll
-        for (int u = 1; u < kBmUnroll / 2; ++u) {
-          a = fmaxf(a, mx[u]);
-          d = fmaxf(d, mx[kBmUnroll / 2 + u]);
-        }
-        int ra = 0, rd = 0;
-        for (int o = 0; o < 32; ++o) {
-          const float x = __shfl_sync(0xffffffffu, a, o), y = __shfl_sync(0xffffffffu, d, o);
-          ra += (x > a || (x == a && o < lane)) + (y > a);
-          rd += (x >= d) + (y > d || (y == d && o < lane));
-        }
-        const unsigned wa = __ballot_sync(0xffffffffu, ra == K - 1), wd = __ballot_sync(0xffffffffu, rd == K - 1);
-        if (wa)
-          c.tz = __shfl_sync(0xffffffffu, a, __ffs(wa) - 1);
-        else if (wd)
-          c.tz = __shfl_sync(0xffffffffu, d, __ffs(wd) - 1);
-        c.tt = c.tz > -INFINITY ? 0x7fffffff : -1;
-        first = false;
-      }
-      // the reference moves at the first finite logit, and then only where
-      // terms would come near fp32's range
-      if (top > ref + 40.f) {
-        const float f = ex2((ref - top) * L);
-        sum *= f;
-        low *= f;
-        ref = top;
-      }
-      const float base_z = ref > -INFINITY ? ref : 0.f;
-      const float2 L2 = make_float2(L, L), nr = make_float2(-base_z, -base_z);
-      float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int u = 0; u < kBmUnroll; ++u)
-#pragma unroll
-        for (int e = 0; e < N; e += 2) {
-          const float2 y = __fmul2_rn(__fadd2_rn(make_float2(z[u][e], z[u][e + 1]), nr), L2);
-          acc = __fadd2_rn(acc, make_float2(ex2(y.x), ex2(y.y)));
-        }
-      {
-        const float x = acc.x + acc.y, s = sum + x, bb = s - sum;
-        low += (sum - (s - bb)) + (x - bb);
-        sum = s;
-      }
-#pragma unroll
-      for (int u = 0; u < kBmUnroll; ++u)
-        if (__any_sync(0xffffffffu, mx[u] >= c.tz && mx[u] > -INFINITY)) gather<N>(c, z[u], base[u], K, lane);
+      for (int i = 0; i < kBmUnroll; ++i)
+        if (i == u) v[i] = t;
     }
-    if (c.cnt > K) prune(c, K, lane);
-    __syncwarp();
-    const float wr = warp_max(ref);
-    const float ws = warp_sum(ref > -INFINITY ? (sum + low) * ex2((ref - wr) * L) : sum);
-    if (lane == 0) {
-      w_ref[warp] = wr;
-      w_sum[warp] = ws;
-      w_cnt[warp] = c.cnt;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      int s = 0;
-      float M = w_ref[0], S = 0.f;
-      for (int w = 0; w < kBmWarps; ++w) {
-        w_at[w] = s;
-        s += w_cnt[w];
-        M = fmaxf(M, w_ref[w]);
-      }
-      w_at[kBmWarps] = s;
-      for (int w = 0; w < kBmWarps; ++w) S += w_ref[w] > -INFINITY ? w_sum[w] * ex2((w_ref[w] - M) * L) : w_sum[w];
-      __stcg(&P.stat[(long long)row * P.spans + sp], make_float4(M, S, S <= 3.4028235e38f ? 0.f : 1.f, 0.f));
-    }
-    __syncthreads();
-    // the warps' candidates by rank
-    const int n = w_at[kBmWarps];
-    BeamCand* out = P.cand + ((long long)row * P.spans + sp) * K;
-    for (int x = tid; x < kBmWarps * K; x += kBmThreads) {
-      const int w = x / K, i = x - w * K;
-      if (i >= w_cnt[w]) continue;
-      const float z = cz[w * kBmCap + i];
-      const int tok = ct[w * kBmCap + i];
-      int rank = 0;
-      for (int w2 = 0; w2 < kBmWarps; ++w2)
-        for (int i2 = 0; i2 < w_cnt[w2]; ++i2) {
-          const float z2 = cz[w2 * kBmCap + i2];
-          rank += z2 > z || (z2 == z && ct[w2 * kBmCap + i2] < tok);
-        }
-      if (rank < K) __stcg(reinterpret_cast<int2*>(out + rank), make_int2(__float_as_int(z), tok));
-    }
-    for (int i = n + tid; i < K; i += kBmThreads)
-      __stcg(reinterpret_cast<int2*>(out + i), make_int2(__float_as_int(-INFINITY), -1));
   }
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) is_last = tagged_arrive(&P.counters[b], P.tag) == P.W * P.spans - 1;
-  __syncthreads();
-  if (!is_last) return;
-  __threadfence();
+}
 
-  // ---- the request's continuations, by the last CTA
-  const int lists = P.W * P.spans;
-  __shared__ double lse[kBeamMax];
-  __shared__ int bad, n_got;
-  __shared__ unsigned long long t_key;
-  __shared__ int t_flat;
-  unsigned long long* hk = reinterpret_cast<unsigned long long*>(smem);  // [lists] heads: order key, flat token
-  int* hf = reinterpret_cast<int*>(hk + lists);
-  unsigned long long* gk = reinterpret_cast<unsigned long long*>(smem + ((size_t)lists * 12 + 15) / 16 * 16);
-  int* gf = reinterpret_cast<int*>(gk + K * K);
+// The sum and the chunks' maxima of a piece, whose first loads are in `next`;
+// the first loads of the piece after it are left there.
+template <typename T>
+__device__ __forceinline__ void beam_piece(const BeamParams& P, BeamShared& sh, const BeamPiece& p,
+                                           const BeamPiece& after, uint4 (&next)[kBmUnroll], float4* stat) {
+  const int row = p.row, lo = p.lo, hi = p.hi;
+  using S = BmShape<T>;
+  constexpr int N = S::N;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float L = 1.4426950408889634f;
+  const T* z0 = static_cast<const T*>(P.logits) + (long long)row * P.ld;
+  float* maxima = P.maxima + (long long)row * P.chunks;
+  // sum + low: the sum with its rounding errors, of 2^(z log2(e) - ref).
+  // References are whole numbers, so that sums move to another one exactly.
+  float ref = -INFINITY, sum = 0.f, low = 0.f, best = -INFINITY;
+  int at = lo + warp * S::kChunk + lane * N;
+  for (int first = lo + warp * S::kChunk; first < hi; first += S::kStep, at += S::kStep) {  // warp-uniform
+    uint4 raw[kBmUnroll];
+#pragma unroll
+    for (int u = 0; u < kBmUnroll; ++u) raw[u] = next[u];
+    beam_fetch<T>(P, p, at + S::kStep, next);
+    const float top = max_of<T>(raw);
+    const uint32_t key = __reduce_max_sync(0xffffffffu, float_key(top));
+    if (lane == 0) __stcg(maxima + first / S::kChunk, key_float(key));
+    best = fmaxf(best, top);
+    // the reference moves at the first finite logit, and then only where
+    // terms would come near fp32's range
+    if (top * L > ref + 60.f) {
+      const float to = ceilf(top * L), f = pow2_int(ref - to);
+      sum *= f;
+      low *= f;
+      ref = to;
+    }
+    const float back = ref > -INFINITY ? -ref : 0.f;
+    const float2 L2 = make_float2(L, L), nr = make_float2(back, back);
+    float2 acc = make_float2(0.f, 0.f), acc2 = acc;
+#pragma unroll
+    for (int u = 0; u < kBmUnroll; ++u) {
+      float z[N];
+      cvt16(raw[u], z);
+#pragma unroll
+      for (int e = 0; e < N; e += 4) {
+        const float2 y = __ffma2_rn(make_float2(z[e], z[e + 1]), L2, nr);
+        const float2 y2 = __ffma2_rn(make_float2(z[e + 2], z[e + 3]), L2, nr);
+        acc = __fadd2_rn(acc, make_float2(ex2(y.x), ex2(y.y)));
+        acc2 = __fadd2_rn(acc2, make_float2(ex2(y2.x), ex2(y2.y)));
+      }
+    }
+    const float x = (acc.x + acc.y) + (acc2.x + acc2.y), s = sum + x, bb = s - sum;
+    low += (sum - (s - bb)) + (x - bb);
+    sum = s;
+  }
+  beam_fetch<T>(P, after, after.lo + warp * S::kChunk + lane * N, next);
+  best = warp_max(best);
+  if (lane == 0) sh.w_top[warp] = best;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kBmWarps; ++w) best = fmaxf(best, sh.w_top[w]);
+  // A piece of nothing but the lowest finite logits (masks): scaled, they
+  // leave fp32's range, so they are summed again relative to their maximum.
+  const bool lowest = best > -INFINITY && best * L == -INFINITY;
+  if (lowest) {
+    ref = 0.f;
+    sum = low = 0.f;
+    for (int v = lo + tid; v < hi; v += kBmThreads) sum += ex2((to_f32<T>(z0[v]) - best) * L);
+  }
+  const float wr = warp_max(ref);
+  const float ws = warp_sum(ref > -INFINITY ? (sum + low) * pow2_int(ref - wr) : sum);
+  if (lane == 0) {
+    sh.w_ref[warp] = wr;
+    sh.w_sum[warp] = ws;
+  }
+  __syncthreads();
   if (tid == 0) {
-    bad = 0;
-    n_got = 0;
-    t_key = 0;
-    t_flat = 0x7fffffff;
+    float M = sh.w_ref[0], sum_all = 0.f;
+    for (int w = 1; w < kBmWarps; ++w) M = fmaxf(M, sh.w_ref[w]);
+    for (int w = 0; w < kBmWarps; ++w)
+      sum_all += sh.w_ref[w] > -INFINITY ? sh.w_sum[w] * pow2_int(sh.w_ref[w] - M) : sh.w_sum[w];
+    __stcg(stat, make_float4(lowest ? best : M, sum_all, sum_all <= 3.4028235e38f ? 0.f : 1.f, lowest ? 1.f : 0.f));
+  }
+}
+
+// As tagged_arrive, by `n` at once.
+__device__ __forceinline__ int tagged_add(unsigned long long* ctr, unsigned long long tag, int n) {
+  const unsigned long long v = *reinterpret_cast<volatile unsigned long long*>(ctr);
+  if ((v >> kTagShift) != tag) atomicCAS(ctr, v, tag << kTagShift);
+  return (int)(atomicAdd(ctr, (unsigned long long)n) & ((1ull << kTagShift) - 1ull));
+}
+
+// The request's candidates in shared memory.
+struct BeamPool {
+  unsigned long long* key;
+  int* flat;
+  int* hot;   // chunks
+};
+
+// The best K of the pool's n candidates, in order, to sh.best; the others go.
+__device__ __forceinline__ void beam_best(BeamShared& sh, const BeamPool& pool, int n, int K) {
+  for (int x = threadIdx.x; x < n; x += kBmThreads) {
+    const unsigned long long k = pool.key[x];
+    const int f = pool.flat[x];
+    int rank = 0;
+#pragma unroll 4
+    for (int y = 0; y < n; ++y) rank += pool.key[y] > k || (pool.key[y] == k && pool.flat[y] < f);
+    if (rank < K) {
+      sh.best_key[rank] = k;
+      sh.best_flat[rank] = f;
+    }
   }
   __syncthreads();
-  for (int w = warp; w < P.W; w += kBmWarps) {
-    const float s0 = P.scores[b * P.W + w];
-    const bool end = P.finished && P.finished[b * P.W + w] != 0;
-    if (!(s0 < INFINITY)) bad = 1;
-    if (end || !(s0 > -INFINITY)) continue;
-    const float4* st = P.stat + (long long)(b * P.W + w) * P.spans;
-    float M = -INFINITY;
-    int off = 0;
-    for (int i = lane; i < P.spans; i += 32) {
-      const float4 v = __ldcg(st + i);
-      off |= v.z != 0.f;
-      if (v.y > 0.f) M = fmaxf(M, v.x);
+}
+
+// A request's continuations; sh.place and sh.pieces are set.
+//
+// A chunk's maximum gives its best score.  Each thread keeps the best of its
+// share of chunks; the K-th best of these 256 bounds the K-th continuation
+// from below, so only chunks at or above it (about K) are read once more.
+template <typename T>
+__device__ __forceinline__ void beam_finish(const BeamParams& P, BeamShared& sh, unsigned char* smem,
+                                            const BeamSplit& sp, int b) {
+  using S = BmShape<T>;
+  constexpr int N = S::N;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = P.keep;
+  const float L = 1.4426950408889634f;
+  BeamPool pool;
+  pool.key = reinterpret_cast<unsigned long long*>(smem);
+  pool.flat = reinterpret_cast<int*>(pool.key + kBmCap);
+  pool.hot = pool.flat + kBmCap;
+  if (tid == 0) sh.bad = sh.n_got = sh.n_hot = sh.over = 0;
+  // Chunks by thread in turn, eight loads at once; the first eight stay.
+  const float* maxima = P.maxima + (long long)b * P.W * P.chunks;
+  constexpr int HELD = 8;
+  const int n_chunk = P.W * P.chunks;
+  float held[HELD];
+  // a chunk's row: exact, as a request has fewer than 2^22 chunks
+  const float inv_chunks = 1.f / (float)P.chunks;
+  auto row_of = [&](int id) { return (int)(((float)id + 0.5f) * inv_chunks); };
+  auto fetch = [&](int from, float (&m)[HELD]) {
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const int id = from + i * kBmThreads;
+      m[i] = id < n_chunk && sh.place[row_of(id)] >= 0 ? __ldcg(maxima + id) : -INFINITY;
     }
-    M = warp_max(M);
-    double S = 0.0;
-    for (int i = lane; i < P.spans; i += 32) {
-      const float4 v = __ldcg(st + i);
-      if (v.y > 0.f) S += (double)v.y * exp2(((double)v.x - (double)M) * (double)L);
+  };
+  fetch(tid, held);
+  __syncthreads();
+  // the rows' sums, by 8 lanes each
+#pragma unroll 1
+  for (int first = 0; first < P.W; first += kBmThreads / 8) {
+    const int w = first + tid / 8, sub = tid & 7;
+    const bool in = w < P.W;
+    const float s0 = in ? P.scores[b * P.W + w] : 0.f;
+    const int a = in ? sh.place[w] : -1, n = a >= 0 ? sh.pieces[w] : 0, cta = a >= 0 ? sp.first_cta(a) : 0;
+    // sums of whole references, and of masks alone
+    float M = -INFINITY, M_low = -INFINITY;
+    double sum = 0.0, sum_low = 0.0;
+    int off = !(s0 < INFINITY);
+#pragma unroll 1
+    for (int i = sub; i < n; i += 32) {
+      float4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = i + 8 * j < n ? __ldcg(P.stat + sp.record(cta + i + 8 * j, a, P.spans)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        off |= v[j].z != 0.f;
+        if (!(v[j].y > 0.f)) continue;
+        if (v[j].w == 0.f) {
+          const float to = fmaxf(M, v[j].x);
+          sum = sum * (double)pow2_int(M - to) + (double)(v[j].y * pow2_int(v[j].x - to));
+          M = to;
+        } else {
+          const float to = fmaxf(M_low, v[j].x);
+          sum_low = sum_low * (double)ex2((M_low - to) * L) + (double)(v[j].y * ex2((v[j].x - to) * L));
+          M_low = to;
+        }
+      }
     }
-    S = warp_sum_d(S);
-    if (warp_or(off) && lane == 0) bad = 1;
-    // an empty row has no reference (and no continuation)
-    if (lane == 0) lse[w] = S > 0.0 ? (double)M + log2(S) / (double)L : 0.0;
+    float M_all = M, low_all = M_low;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      M_all = fmaxf(M_all, __shfl_xor_sync(0xffffffffu, M_all, o));
+      low_all = fmaxf(low_all, __shfl_xor_sync(0xffffffffu, low_all, o));
+    }
+    const bool low_row = !(M_all > -INFINITY);  // nothing but the lowest logits
+    if (low_row)
+      sum = M_low > -INFINITY ? sum_low * (double)ex2((M_low - low_all) * L) : 0.0;
+    else
+      sum = M > -INFINITY ? sum * (double)pow2_int(M - M_all) : 0.0;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (off) sh.bad = 1;
+    if (in && sub == 0) {
+      sh.s0[w] = s0;
+      sh.row_sum[w] = sum;
+      sh.row_ref[w] = low_row ? low_all : M_all;
+      sh.row_low[w] = low_row;
+    }
   }
   __syncthreads();
-  if (bad) {
+  // log2 of a sum: its exponent, log2f of its fp32 fraction in [1, 2) (off by
+  // 2^-24 at most) and the fraction's rounding.  log2(e) is the fp32 constant
+  // by which logits were scaled; an empty row has no sum (and no
+  // continuation).  In fp32 a score is z + add, off by less than err plus
+  // 2^-22 |z|.
+  for (int w = tid; w < P.W; w += kBmThreads) {
+    double l2 = 0.0;
+    if (sh.row_sum[w] > 0.0) {
+      const long long bits = __double_as_longlong(sh.row_sum[w]);
+      const double m = __longlong_as_double((bits & 0x000fffffffffffffll) | 0x3ff0000000000000ll);
+      const float mf = (float)m;
+      l2 = (double)((int)(bits >> 52) - 1023) + (double)log2f(mf) + (double)((float)(m - (double)mf) / mf * L);
+    }
+    constexpr double inv = 1.0 / 1.4426950216293335;  // of that constant
+    const double lse = sh.row_low[w] ? (double)sh.row_ref[w] + l2 * inv : ((double)sh.row_ref[w] + l2) * inv;
+    const float s0 = sh.s0[w];
+    sh.lse[w] = lse;
+    sh.add[w] = (float)((double)s0 - lse);
+    sh.err[w] = 4.8e-7f * fabsf((float)((double)s0 - lse));
+  }
+  __syncthreads();
+  if (sh.bad) {
     for (int i = tid; i < K; i += kBmThreads) {
       P.out_scores[b * K + i] = -INFINITY;
       P.out_parents[b * K + i] = -1;
@@ -330,80 +436,263 @@ __global__ void __launch_bounds__(kBmThreads) beam_select_kernel(const BeamParam
     if (tid == 0 && P.status) P.status[b] = kStatusBadLogits;
     return;
   }
-  // The score of entry i of a list; key 0: none.  (A score's key is above 0.)
-  auto entry = [&](int list, int i, int& flat) -> unsigned long long {
-    const int w = list / P.spans;
-    const float s0 = P.scores[b * P.W + w];
-    flat = 0x7fffffff;
-    if (!(s0 > -INFINITY)) return 0ull;
-    if (P.finished && P.finished[b * P.W + w] != 0) {
-      if (i > 0 || list != w * P.spans) return 0ull;
-      flat = w * P.V + P.end_token;
-      return double_key((double)s0);
-    }
-    const int2 v = __ldcg(reinterpret_cast<const int2*>(P.cand + ((long long)b * lists + list) * K + i));
-    if (v.y < 0) return 0ull;
-    flat = w * P.V + v.y;
-    return double_key((double)s0 + ((double)__int_as_float(v.x) - lse[w]));
+  float best = -INFINITY;
+  auto take = [&](int from, const float (&m)[HELD]) {
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (m[i] > -INFINITY) {
+        const int w = row_of(from + i * kBmThreads);
+        best = fmaxf(best, (m[i] + sh.add[w]) - (sh.err[w] + 2.4e-7f * fabsf(m[i])));
+      }
   };
-  for (int i = tid; i < lists; i += kBmThreads) {
-    int f;
-    hk[i] = entry(i, 0, f);
-    hf[i] = f;
+  take(tid, held);
+  for (int from = tid + HELD * kBmThreads; from < n_chunk; from += HELD * kBmThreads) {
+    float m[HELD];
+    fetch(from, m);
+    take(from, m);
+  }
+  sh.t_max[tid] = best;
+  __syncthreads();
+  const float floor = kth_bound(sh.t_max, K, lane);
+  // from below, what a logit of each row has to be to score `floor`
+  for (int w = tid; w < P.W; w += kBmThreads) {
+    const float z = floor - sh.add[w];
+    sh.z_min[w] = z - (sh.err[w] + 4.8e-7f * (fabsf(z) + fabsf(floor)));
   }
   __syncthreads();
-  // K lists' heads are at or above the K-th best head, so no entry below it is kept
-  for (int i = tid; i < lists; i += kBmThreads) {
-    const unsigned long long k = hk[i];
-    const int f = hf[i];
-    if (k == 0ull) continue;
-    int rank = 0;
-    for (int x = 0; x < lists; ++x) rank += hk[x] > k || (hk[x] == k && hf[x] < f);
-    if (rank == K - 1) {
-      t_key = k;
-      t_flat = f;
+  for (int w = tid; w < P.W; w += kBmThreads) {  // an ended beam goes on as it is
+    if (sh.place[w] < 0 && sh.s0[w] > -INFINITY && P.finished && P.finished[b * P.W + w] != 0) {
+      const int to = atomicAdd(&sh.n_got, 1);
+      pool.key[to] = double_key((double)sh.s0[w]);
+      pool.flat[to] = w * P.V + P.end_token;
     }
   }
-  __syncthreads();
-  const unsigned long long tk = t_key;
-  const int tf = t_flat;
-  for (int x = tid; x < lists * K; x += kBmThreads) {
-    const int list = x / K, i = x - list * K;
-    const unsigned long long hk0 = hk[list];
-    if (hk0 == 0ull || hk0 < tk || (hk0 == tk && hf[list] > tf)) continue;
-    int f;
-    const unsigned long long k = entry(list, i, f);
-    if (k == 0ull || k < tk || (k == tk && f > tf)) continue;
-    const int to = atomicAdd(&n_got, 1);  // at most K lists of K entries
-    gk[to] = k;
-    gf[to] = f;
+  auto mark = [&](int from, const float (&m)[HELD]) {
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (m[i] > -INFINITY && m[i] >= sh.z_min[row_of(from + i * kBmThreads)]) {
+        const int to = atomicAdd(&sh.n_hot, 1);
+        if (to < kBmHot) pool.hot[to] = from + i * kBmThreads;
+      }
+  };
+  mark(tid, held);
+  for (int from = tid + HELD * kBmThreads; from < n_chunk; from += HELD * kBmThreads) {
+    float m[HELD];
+    fetch(from, m);
+    mark(from, m);
   }
   __syncthreads();
-  const int n = n_got;
-  for (int x = tid; x < n; x += kBmThreads) {
-    const unsigned long long k = gk[x];
-    const int f = gf[x];
-    int rank = 0;
-    for (int y = 0; y < n; ++y) rank += gk[y] > k || (gk[y] == k && gf[y] < f);
-    if (rank < K) {
-      P.out_scores[b * K + rank] = (float)key_double(k);
-      P.out_parents[b * K + rank] = f / P.V;
-      P.out_tokens[b * K + rank] = f % P.V;
+  const int n_hot = sh.n_hot, n_ended = sh.n_got;
+  __syncthreads();
+  const T* logits = static_cast<const T*>(P.logits) + (long long)b * P.W * P.ld;
+  // adds a chunk's u-th vector's tokens at or above their row's z_min and the
+  // bound (tk, tf); the code is run once by a CTA, so it is kept short
+  unsigned long long tk = 0ull;
+  int tf = 0x7fffffff;
+  auto add_vector = [&](int w, int tok, const uint4& raw) {
+    float z[N];
+    cvt16(raw, z);
+    unsigned in = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) in |= (z[e] >= sh.z_min[w] && z[e] > -INFINITY ? 1u : 0u) << e;
+    while (in) {
+      const int t = tok + __ffs(in) - 1;
+      in &= in - 1;
+      const double zt = (double)to_f32<T>(logits[(long long)w * P.ld + t]);
+      const unsigned long long k = double_key((double)sh.s0[w] + (zt - sh.lse[w]));
+      const int f = w * P.V + t;
+      if (k < tk || (k == tk && f > tf)) continue;
+      const int to = atomicAdd(&sh.n_got, 1);
+      if (to >= kBmCap) {
+        sh.over = 1;
+      } else {
+        pool.key[to] = k;
+        pool.flat[to] = f;
+      }
+    }
+  };
+  if (n_hot <= kBmHot) {
+    uint4 ahead[kBmUnroll];
+    int w_next = 0, tok_next = 0;
+    auto chunk = [&](int i) {  // the loads of the i-th
+      if (i >= n_hot) return;
+      const int id = pool.hot[i];
+      BeamPiece p;
+      w_next = row_of(id);
+      tok_next = (id - w_next * P.chunks) * S::kChunk + lane * N;
+      p.row = b * P.W + w_next;
+      p.hi = P.V;
+      beam_fetch<T>(P, p, tok_next, ahead);
+    };
+    chunk(warp);
+#pragma unroll 1
+    for (int i = warp; i < n_hot; i += kBmWarps) {
+      uint4 v[kBmUnroll];
+#pragma unroll
+      for (int u = 0; u < kBmUnroll; ++u) v[u] = ahead[u];
+      const int w = w_next, tok = tok_next;
+      chunk(i + kBmWarps);
+#pragma unroll 1
+      for (int u = 0; u < kBmUnroll; ++u) {
+        add_vector(w, tok + u * 32 * N, v[0]);
+#pragma unroll
+        for (int j = 0; j + 1 < kBmUnroll; ++j) v[j] = v[j + 1];
+      }
+    }
+  } else if (tid == 0) {
+    sh.over = 1;
+  }
+  __syncthreads();
+  int n = min(sh.n_got, kBmCap);
+  if (sh.over) {
+    // Too many at the bound (long runs of equal logits): chunk by chunk in
+    // order, with the K-th best so far as the bound, ties by place.
+    __syncthreads();
+    if (tid == 0) sh.n_got = n_ended;
+    __syncthreads();
+    if (tid == 0) sh.over = 0;
+#pragma unroll 1
+    for (int id = 0; id < n_chunk; ++id) {
+      const int row = row_of(id);
+      if (sh.place[row] < 0) continue;
+      const float m = __ldcg(maxima + id);
+      if (!(m > -INFINITY && m >= sh.z_min[row])) continue;
+      if (warp < kBmUnroll) {  // at most kBmCap - kChunk candidates before
+        const int tok = (id - row * P.chunks) * S::kChunk + (warp * 32 + lane) * N;
+        add_vector(row, tok, load_tail<T>(logits + (long long)row * P.ld, tok, P.V));
+      }
+      __syncthreads();
+      n = sh.n_got;
+      __syncthreads();
+      if (n > kBmCap - S::kChunk) {
+        beam_best(sh, pool, n, K);
+        for (int i = tid; i < K; i += kBmThreads) {
+          pool.key[i] = sh.best_key[i];
+          pool.flat[i] = sh.best_flat[i];
+        }
+        tk = sh.best_key[K - 1];
+        tf = sh.best_flat[K - 1];
+        if (tid == 0) sh.n_got = K;
+        __syncthreads();
+        n = K;
+      }
     }
   }
-  for (int i = n + tid; i < K; i += kBmThreads) {
-    P.out_scores[b * K + i] = -INFINITY;
-    P.out_parents[b * K + i] = -1;
-    P.out_tokens[b * K + i] = -1;
+  beam_best(sh, pool, n, K);
+  for (int i = tid; i < K; i += kBmThreads) {
+    const bool in = i < n;
+    P.out_scores[b * K + i] = in ? (float)key_double(sh.best_key[i]) : -INFINITY;
+    P.out_parents[b * K + i] = in ? sh.best_flat[i] / P.V : -1;
+    P.out_tokens[b * K + i] = in ? sh.best_flat[i] % P.V : -1;
   }
   if (tid == 0 && P.status) P.status[b] = 0;
 }
 
-size_t beam_smem(const BeamParams& P) {
-  const size_t lists = (size_t)P.W * P.spans;
-  const size_t a = (size_t)kBmWarps * kBmCap * 8;
-  const size_t m = (lists * 12 + 15) / 16 * 16 + (size_t)P.keep * P.keep * 12;
-  return a > m ? a : m;
+// One wave of CTAs, each with an even share of all logits that are read; the
+// last CTA of a request to arrive picks its continuations.
+template <typename T>
+__global__ void __launch_bounds__(kBmThreads, kBmCtas) beam_select_kernel(const BeamParams P) {
+  using S = BmShape<T>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ BeamShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = P.B * P.W;
+  BeamSplit sp;
+  sp.steps = (P.V + S::kStep - 1) / S::kStep;
+  if (R <= kBeamRows) {
+    int* rows = reinterpret_cast<int*>(smem + kBmCap * 12 + kBmHot * 4);
+    int n = 0;
+    for (int base = 0; base < R; base += kBmThreads) {
+      const int r = base + tid;
+      const bool in = r < R && beam_read(P, r);
+      const unsigned who = __ballot_sync(0xffffffffu, in);
+      if (lane == 0) sh.w_cnt[warp] = __popc(who);
+      __syncthreads();
+      int at = n;
+      for (int w = 0; w < kBmWarps; ++w) {
+        if (w < warp) at += sh.w_cnt[w];
+        n += sh.w_cnt[w];
+      }
+      if (in) rows[at + __popc(who & ((1u << lane) - 1u))] = r;
+      __syncthreads();
+    }
+    sp.rows = rows;
+    sp.n = n;
+  } else {
+    sp.rows = nullptr;
+    sp.n = R;
+  }
+  sp.total = (long long)sp.n * sp.steps;
+  sp.used = (int)min((long long)gridDim.x, sp.total);
+  sp.small = (sp.total + 1) * (sp.used + 1) < (1ll << 32);
+  const int cta = blockIdx.x;
+  // the places and pieces of request b's rows; `near`: the place of one
+  auto request = [&](int b, int near) {
+    for (int w = tid; w < P.W; w += kBmThreads) sh.place[w] = -1;
+    __syncthreads();
+    const int a = near - kBeamMax + tid;
+    if (tid < 2 * kBeamMax && a >= 0 && a < sp.n) {
+      const int w = sp.row(a) - b * P.W;
+      if (w >= 0 && w < P.W) {
+        sh.pieces[w] = sp.pieces(a);
+        sh.place[w] = sp.rows || beam_read(P, sp.row(a)) ? a : -1;
+      }
+    }
+    __syncthreads();
+  };
+  if (cta < sp.used) {
+    long long x = sp.begin(cta);
+    const long long end = sp.begin(cta + 1);
+    // the piece at step y (of no tokens past the range)
+    auto piece = [&](long long y) {
+      BeamPiece p;
+      p.a = (int)((uint32_t)y / (uint32_t)sp.steps);
+      p.row = y < end ? sp.row(p.a) : 0;
+      const int c0 = (int)(y - (long long)p.a * sp.steps), len = (int)min((long long)(sp.steps - c0), end - y);
+      p.lo = c0 * S::kStep;
+      p.hi = y < end ? (int)min((long long)P.V, (long long)(c0 + len) * S::kStep) : 0;
+      return p;
+    };
+    BeamPiece p = piece(x);
+    uint4 next[kBmUnroll];
+    beam_fetch<T>(P, p, p.lo + warp * S::kChunk + lane * S::N, next);
+    while (x < end) {
+      const int b = p.row / P.W, len = (p.hi - p.lo + S::kStep - 1) / S::kStep;
+      const BeamPiece after = piece(x + len);
+      if (sp.rows || beam_read(P, p.row))
+        beam_piece<T>(P, sh, p, after, next, P.stat + sp.record(cta, p.a, P.spans));
+      else
+        beam_fetch<T>(P, after, after.lo + warp * S::kChunk + lane * S::N, next);
+      // A request's arrivals count steps: its rows in the split have so many.
+      const int a = p.a - kBeamMax + tid;
+      const bool its = tid < 2 * kBeamMax && a >= 0 && a < sp.n && sp.row(a) >= b * P.W && sp.row(a) < (b + 1) * P.W;
+      const int rows = __syncthreads_count(its);  // and what the CTA has written is before this
+      if (tid == 0) {
+        __threadfence();
+        sh.is_last = tagged_add(&P.counters[b], P.tag, len) + len == rows * sp.steps;
+      }
+      __syncthreads();
+      if (sh.is_last) {
+        __threadfence();
+        request(b, p.a);
+        beam_finish<T>(P, sh, smem, sp, b);
+        __syncthreads();
+      }
+      x += len;
+      p = after;
+    }
+  }
+  // requests without a row in the split
+  if (sp.rows) {
+    for (int b = cta; b < P.B; b += gridDim.x) {
+      bool some = false;
+      for (int w = tid; w < P.W; w += kBmThreads) some |= beam_read(P, b * P.W + w);
+      if (__syncthreads_or(some)) continue;
+      for (int w = tid; w < P.W; w += kBmThreads) sh.place[w] = -1;
+      __syncthreads();
+      beam_finish<T>(P, sh, smem, sp, b);
+      __syncthreads();
+    }
+  }
 }
 
 // ---------------------------------------------------------- reordering
@@ -451,34 +740,28 @@ __global__ void __launch_bounds__(kRoThreads) beam_reorder_kernel(const ReorderP
 
 }  // namespace
 
-// Spans of a row: enough CTAs to fill the device a few times over, each with
-// at least one step of every thread.
-int beam_spans(int rows, int V, int num_sms) {
-  const int step = kBmThreads * 8 * kBmUnroll;
-  const int want = (4 * num_sms + rows - 1) / rows, most = (V + step - 1) / step;
-  return want < most ? want : most;
-}
-
-int beam_smem_bytes(int W, int spans, int keep) {
-  BeamParams P{};
-  P.W = W;
-  P.spans = spans;
-  P.keep = keep;
-  return (int)beam_smem(P);
+// The launch: as many CTAs as the device holds at once, of at least one step
+// each.  P.spans becomes the most pieces of a CTA, P.chunks a row's chunks.
+void plan_beams(BeamParams& P, bool bf16, int num_sms) {
+  const int chunk = bf16 ? BmShape<__nv_bfloat16>::kChunk : BmShape<float>::kChunk;
+  const long long step = (long long)kBmWarps * chunk, steps = (P.V + step - 1) / step, rows = (long long)P.B * P.W;
+  long long g = (long long)kBmCtas * num_sms;
+  if (g > rows * steps) g = rows * steps;
+  P.grid = (int)g;
+  P.chunks = (P.V + chunk - 1) / chunk;
+  // a CTA's range is at most this many steps, whichever rows are read
+  const long long range = (rows * steps + g - 1) / g;
+  P.spans = (int)((range + steps - 1) / steps + 1);
 }
 
 int launch_beam_select(const BeamParams& P, bool bf16, cudaStream_t s) {
-  const int bytes = (int)beam_smem(P);
-  const unsigned grid = (unsigned)((long long)P.B * P.W * P.spans);
-  const void* f = bf16 ? (const void*)beam_select_kernel<__nv_bfloat16> : (const void*)beam_select_kernel<float>;
-  if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
-    cudaGetLastError();
-    return -1;
-  }
+  // the last CTA's candidates and chunks, then the rows that are read
+  const long long rows = (long long)P.B * P.W;
+  const int bytes = kBmCap * 12 + kBmHot * 4 + (rows <= kBeamRows ? (int)rows * 4 : 0);
   if (bf16)
-    beam_select_kernel<__nv_bfloat16><<<grid, kBmThreads, bytes, s>>>(P);
+    beam_select_kernel<__nv_bfloat16><<<P.grid, kBmThreads, bytes, s>>>(P);
   else
-    beam_select_kernel<float><<<grid, kBmThreads, bytes, s>>>(P);
+    beam_select_kernel<float><<<P.grid, kBmThreads, bytes, s>>>(P);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 

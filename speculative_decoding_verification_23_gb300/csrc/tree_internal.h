@@ -119,12 +119,6 @@ struct CommitParams {
 // ----------------------------------------------------------------- beams
 constexpr int kBeamMax = 64;      // beams per request, and beams kept
 
-// A continuation of one span: the logit and its token.
-struct BeamCand {
-  float z;
-  int tok;
-};
-
 struct BeamParams {
   const void* logits;
   long long ld;
@@ -136,21 +130,22 @@ struct BeamParams {
   int32_t* status;
   unsigned long long* counters;  // [B] arrivals, call-tagged
   unsigned long long tag;
-  float4* stat;                  // [B * W * spans] (reference, sum, bad, -)
-  BeamCand* cand;                // [B * W * spans][keep]
-  int B, W, keep, V, end_token, spans, span;  // span: tokens per span
+  float4* stat;                  // [grid * spans] (reference, sum, bad, of masks alone)
+  float* maxima;                 // [B * W][chunks]
+  int B, W, keep, V, end_token;
+  int grid, spans, chunks;       // CTAs, the most pieces of rows in one, chunks of a row
 };
 
 struct BeamWorkspace {
-  size_t off_counters, off_stat, off_cand, total;
+  size_t off_counters, off_stat, off_maxima, total;
 };
 
-inline BeamWorkspace make_beam_workspace(int B, int W, int spans, int keep) {
+inline BeamWorkspace make_beam_workspace(int B, int W, int grid, int spans, int chunks) {
   BeamWorkspace w;
   w.off_counters = 0;
   w.off_stat = up256((size_t)B * 8);
-  w.off_cand = w.off_stat + up256((size_t)B * W * spans * 16);
-  w.total = w.off_cand + up256((size_t)B * W * spans * keep * sizeof(BeamCand));
+  w.off_maxima = w.off_stat + up256((size_t)grid * spans * 16);
+  w.total = w.off_maxima + up256((size_t)B * W * chunks * 4);
   return w;
 }
 

@@ -22,8 +22,7 @@ int launch_tree_join(const TreeParams& P, bool bf16, int num_sms, cudaStream_t s
 int launch_weigh(const WeighParams& P, bool bf16, int num_sms, cudaStream_t s);
 int launch_evict(const EvictParams& P, cudaStream_t s);
 int launch_commit(const CommitParams& P, cudaStream_t s);
-int beam_spans(int rows, int V, int num_sms);
-int beam_smem_bytes(int W, int spans, int keep);
+void plan_beams(BeamParams& P, bool bf16, int num_sms);
 int launch_beam_select(const BeamParams& P, bool bf16, cudaStream_t s);
 long long plan_reorder(ReorderParams& P);
 int launch_beam_reorder(const ReorderParams& P, long long blocks, cudaStream_t s);
@@ -347,12 +346,25 @@ int check_beams(const spec_beam_args* a) {
   if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
   if (a->B < 1 || a->V < 1 || a->W < 1 || a->W > SPEC_MAX_BEAMS || a->keep < 1 || a->keep > SPEC_MAX_BEAMS)
     return SPEC_ERR_SHAPE;
-  if ((long long)a->W * a->V > INT32_MAX || (long long)a->B * a->W > INT32_MAX / 4096) return SPEC_ERR_SHAPE;
+  // places in the split of the logits and of a request's candidates are 32-bit
+  if ((long long)a->W * a->V > INT32_MAX / 2 || (long long)a->B * a->W > INT32_MAX / 4096 ||
+      (long long)a->B * a->W * ((a->V + 4095ll) / 4096) > INT32_MAX)
+    return SPEC_ERR_SHAPE;
   if (!a->logits || !a->scores) return SPEC_ERR_NULL;
   if (a->ld < a->V) return SPEC_ERR_SHAPE;
   if (a->finished && (a->end_token < 0 || a->end_token >= a->V)) return SPEC_ERR_SHAPE;
   if (!aligned16(a->logits) || (a->ld * (a->dtype == SPEC_BF16 ? 2 : 4)) % 16 != 0) return SPEC_ERR_ALIGN;
   return SPEC_OK;
+}
+
+void beam_params(sv::BeamParams& P, const spec_beam_args* a, int num_sms) {
+  std::memset(&P, 0, sizeof(P));
+  P.B = a->B;
+  P.W = a->W;
+  P.keep = a->keep;
+  P.V = a->V;
+  P.end_token = a->end_token;
+  sv::plan_beams(P, a->dtype == SPEC_BF16, num_sms);
 }
 
 // Tags of the calls whose kernels count arrivals (see tagged_arrive), as in
@@ -386,7 +398,9 @@ size_t spec_beam_workspace_bytes(const spec_beam_args* a) {
   if (check_beams(a)) return 0;
   int sms = kPlanSms;
   if (sm_count(&sms)) sms = kPlanSms;
-  return sv::make_beam_workspace(a->B, a->W, sv::beam_spans(a->B * a->W, a->V, sms), a->keep).total;
+  sv::BeamParams P;
+  beam_params(P, a, sms);
+  return sv::make_beam_workspace(a->B, a->W, P.grid, P.spans, P.chunks).total;
 }
 
 int spec_beam_select(const spec_beam_args* a, float* out_scores, int32_t* out_parents, int32_t* out_tokens,
@@ -399,9 +413,8 @@ int spec_beam_select(const spec_beam_args* a, float* out_scores, int32_t* out_pa
   int sms = 0;
   rc = sm_count(&sms);
   sv::BeamParams P;
-  std::memset(&P, 0, sizeof(P));
-  P.spans = sv::beam_spans(a->B * a->W, a->V, rc ? kPlanSms : sms);
-  const sv::BeamWorkspace W = sv::make_beam_workspace(a->B, a->W, P.spans, a->keep);
+  beam_params(P, a, rc ? kPlanSms : sms);
+  const sv::BeamWorkspace W = sv::make_beam_workspace(a->B, a->W, P.grid, P.spans, P.chunks);
   if (ws_bytes < W.total) return SPEC_ERR_WORKSPACE;
   if (rc) return rc;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -416,13 +429,7 @@ int spec_beam_select(const spec_beam_args* a, float* out_scores, int32_t* out_pa
   P.status = out_status;
   P.counters = reinterpret_cast<unsigned long long*>(w + W.off_counters);
   P.stat = reinterpret_cast<float4*>(w + W.off_stat);
-  P.cand = reinterpret_cast<sv::BeamCand*>(w + W.off_cand);
-  P.B = a->B;
-  P.W = a->W;
-  P.keep = a->keep;
-  P.V = a->V;
-  P.end_token = a->end_token;
-  P.span = ((a->V + P.spans - 1) / P.spans + 7) / 8 * 8;
+  P.maxima = reinterpret_cast<float*>(w + W.off_maxima);
   rc = beam_tag(P.counters, a->B, s, &P.tag);
   if (rc) return rc;
   return sv::launch_beam_select(P, a->dtype == SPEC_BF16, s) == 0 ? SPEC_OK : SPEC_ERR_LAUNCH;
