@@ -296,10 +296,17 @@ __global__ void __launch_bounds__(kWtWarps * 32, WtShape<D>::kCtas) tree_warp_ke
 // item: lane l the row l % 8 and channels 4 (l / 8) .. + 3 of every 16, so
 // that pieces are read by 128 bytes and results written by 32.  Also the
 // status of every request, and NaN in the rows of one whose lengths are bad.
-constexpr int kJoinWarps = 4;
+//
+// A few pieces of an item are read by one warp; many (a long context of few
+// heads) by all warps of the CTA, a share each, whose sums are added in warp
+// order.
+template <int D>
+constexpr int kJoinOf = D <= 128 ? 8 : 4;  // warps: their sums fit 48 KB of shared memory
+constexpr int kJoinFew = 6;  // pieces that one warp reads
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeParams P) {
+__global__ void __launch_bounds__(kJoinOf<D> * 32) tree_join_kernel(const TreeParams P) {
+  constexpr int kJoinWarps = kJoinOf<D>;
   const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const TreeReq r = tree_request(P, b);
   const int heads_q = P.heads * P.group;
@@ -337,37 +344,94 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
   const long long T_ = P.start[P.B], s0 = P.start[b];
   const int used = tree_used(P, T_);
   const int rows = r.n * P.group, blocks = (rows + 7) / 8;  // P.rows is a multiple of 8
-  for (int i = blockIdx.y * kJoinWarps + warp; i < blocks * P.heads; i += gridDim.y * kJoinWarps) {
+  if (rows == 0) return;
+  // most pieces of an item of this request
+  const int most = (int)(((long long)r.per_item * used + T_ - 1) / T_) + 1;
+  const bool many = most > kJoinFew;
+  const int step = many ? gridDim.y : gridDim.y * kJoinWarps;
+  __shared__ float4 part[kJoinWarps][D / 16][32];
+  __shared__ float2 part_ml[kJoinWarps][8];
+  for (int i = many ? blockIdx.y : blockIdx.y * kJoinWarps + warp; i < blocks * P.heads; i += step) {
     const int kvh = i / blocks, R0 = (i - kvh * blocks) * 8;
     const long long s = s0 + ((long long)kvh * r.mb + R0 / P.rows) * r.per_item;
     const int c0 = tree_owner(s, T_, used), c1 = tree_owner(s + r.per_item - 1, T_, used);
     if (c0 == c1) continue;  // written whole
     const bool in = R0 + sub < rows;
     const int row = R0 % P.rows + (in ? sub : 0);
-    // CTA c0 in slot 1, c0 + 1 .. c1 in slot 0
-    float M = -INFINITY;
-    for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(&P.part_ml[(2ll * c + (c == c0)) * P.rows + row]).x);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
+    // CTA c0 in slot 1, c0 + 1 .. c1 in slot 0; a running reference as in the
+    // main kernel, four pieces' loads at once
+    float M = -INFINITY, L = 0.f;
     float4 acc[D / 16];
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) {
-      const long long at = 2ll * c + (c == c0);
-      const float2 ml = __ldcg(&P.part_ml[at * P.rows + row]);
-      const float f = ex2(ml.x - ref);
-      L += ml.y * f;
-      const float4* src = reinterpret_cast<const float4*>(P.part_o) + (at * (D / 4) + quad) * P.rows + row;
+    const int by = many ? kJoinWarps : 1;
+    constexpr int U = D <= 64 ? 4 : (D <= 128 ? 2 : 1);
+    for (int c = c0 + (many ? warp : 0); c <= c1; c += U * by) {
+      float2 ml[U];
+      float4 v[U][D / 16];
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const float4 v = __ldcg(src + (long long)k * 4 * P.rows);
-        acc[k].x += v.x * f;
-        acc[k].y += v.y * f;
-        acc[k].z += v.z * f;
-        acc[k].w += v.w * f;
+      for (int u = 0; u < U; ++u) {
+        const int cu = c + u * by;
+        const long long at = 2ll * cu + (cu == c0);
+        ml[u] = cu <= c1 ? __ldcg(&P.part_ml[at * P.rows + row]) : make_float2(-INFINITY, 0.f);
+        const float4* src = reinterpret_cast<const float4*>(P.part_o) + (at * (D / 4) + quad) * P.rows + row;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          v[u][k] = cu <= c1 ? __ldcg(src + (long long)k * 4 * P.rows) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float to = fmaxf(M, ml[u].x), ref = to == -INFINITY ? 0.f : to;
+        const float f = ex2(M - ref), h = ex2(ml[u].x - ref);
+        L = L * f + ml[u].y * h;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          acc[k].x = acc[k].x * f + v[u][k].x * h;
+          acc[k].y = acc[k].y * f + v[u][k].y * h;
+          acc[k].z = acc[k].z * f + v[u][k].z * h;
+          acc[k].w = acc[k].w * f + v[u][k].w * h;
+        }
+        M = to;
       }
     }
+    if (many) {
+      __syncthreads();  // the last block's sums have been read
+      if (quad == 0) part_ml[warp][sub] = make_float2(M, L);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) part[warp][k][lane] = acc[k];
+      __syncthreads();
+      // channels by warp: a warp adds the sums of D / 16 / kJoinWarps vectors (or one, by some)
+      M = -INFINITY;
+      for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, part_ml[w][sub].x);
+      const float ref = M == -INFINITY ? 0.f : M;
+      L = 0.f;
+      for (int w = 0; w < kJoinWarps; ++w) L += part_ml[w][sub].y * ex2(part_ml[w][sub].x - ref);
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const int R = R0 + sub, node = in ? R / P.group : 0, head = kvh * P.group + (in ? R - node * P.group : 0);
+      T* dst = out + (long long)(r.cu + node) * P.so_node + (long long)head * P.so_head + quad * 4;
+      for (int k = warp; k < D / 16; k += kJoinWarps) {
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < kJoinWarps; ++w) {
+          const float h = ex2(part_ml[w][sub].x - ref);
+          const float4 v = part[w][k][lane];
+          t.x += v.x * h;
+          t.y += v.y * h;
+          t.z += v.z * h;
+          t.w += v.w * h;
+        }
+        if (in) {
+          uint2 o;
+          o.x = pack2<T>(t.x * inv, t.y * inv);
+          o.y = pack2<T>(t.z * inv, t.w * inv);
+          *reinterpret_cast<uint2*>(dst + k * 16) = o;
+        }
+      }
+      if (in && P.lse && warp == 0 && quad == 0)
+        P.lse[(long long)(r.cu + node) * heads_q + head] = L == 0.f ? -INFINITY : (ref + log2f(L)) * kLn2;
+      continue;
+    }
     if (!in) continue;
+    const float ref = M == -INFINITY ? 0.f : M;
     const int R = R0 + sub, node = R / P.group, head = kvh * P.group + R - node * P.group;
     const float inv = L == 0.f ? 0.f : 1.f / L;
     T* dst = out + (long long)(r.cu + node) * P.so_node + (long long)head * P.so_head + quad * 4;
@@ -425,14 +489,13 @@ int launch_tree_warp(const TreeParams& P, bool bf16, cudaStream_t s) {
 namespace {
 template <typename T, int D>
 int launch_join(const TreeParams& P, int num_sms, cudaStream_t s) {
-  // CTAs for every 8 rows of the largest request, and no more than the device
-  // holds at once; they start while the main kernel ends and wait for it there
-  const long long rows = (long long)P.max_nodes * P.group, warps = (rows + 7) / 8 * P.heads;
-  const long long want = (warps + kJoinWarps - 1) / kJoinWarps;
-  const long long most = (12ll * num_sms + P.B - 1) / P.B;
+  // A CTA for every 8 rows of the largest request, up to six per SM in all;
+  // they start while the main kernel ends and wait for it there.
+  const long long rows = (long long)P.max_nodes * P.group, want = (rows + 7) / 8 * P.heads;
+  const long long most = (6ll * num_sms + P.B - 1) / P.B;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(P.B, (unsigned)max(1ll, min(want, most)));
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.blockDim = dim3(kJoinOf<D> * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

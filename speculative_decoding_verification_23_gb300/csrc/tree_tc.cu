@@ -273,52 +273,73 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
 
   if (warp == 4 * NT) {
     // ------------------------------------------------------------ copies
+    // A lane has one box of a tile (at most 16 boxes of 8 slots or more, HD
+    // halves each).  The pages of the tile ahead are looked up before this
+    // one is copied, also where it is the first of another segment.
+    struct Copy {
+      TcTile x;
+      int kvh, row, seg, page, slot;  // row: of the first drafted token
+      bool any;
+    };
     RingFills fills;
     const PageDiv pd(P.page_size);
+    const int bx = lane / HD, half = lane % HD;
+    int seg = -1, t = 0;
+    g.t1 = 0;
+    auto ahead = [&]() {
+      Copy c;
+      c.any = true;
+      c.page = c.slot = 0;
+      if (t >= g.t1) {
+        c.any = walk.next(P, g);
+        ++seg;
+        t = g.t0;
+      }
+      if (!c.any) return c;
+      c.x = tc_tile(walk.r, t++);
+      c.kvh = g.kvh;
+      c.seg = seg;
+      c.row = walk.r.cu + c.x.lo;
+      if (c.x.cached && bx * box < c.x.valid) {
+        int page;
+        pd.split(c.x.lo + bx * box, page, c.slot);
+        c.page = P.table[(long long)g.b * P.ld_table + page];
+      }
+      return c;
+    };
     bool ok = true;
-    for (int seg = 0; ok && walk.next(P, g); ++seg) {
-      for (int t = g.t0; ok && t < g.t1; ++t, ++tc) {
-        const TcTile x = tc_tile(walk.r, t);
-        const int rows = x.cached ? box : kNewBox, nb = (x.valid + rows - 1) / rows;
-        const uint32_t bytes = (uint32_t)(nb * rows * 128 * HD);
-        // boxes of a tile by lane (at most 16 boxes of 8 slots, HD halves each)
-        int page[2], slot[2];
+    int s = 0;
+    uint32_t ph = 0;
+    Copy cur = ahead();
+    while (ok && cur.any) {
+      const Copy next = ahead();
+      const int rows = cur.x.cached ? box : kNewBox, nb = (cur.x.valid + rows - 1) / rows;
+      const uint32_t bytes = (uint32_t)(nb * rows * 128 * HD);
+      if (cur.page < 0 || cur.page >= P.num_pages) {
+        cur.page = 0;
+        bad_seg[cur.seg & 15] = cur.seg;
+      }
+      __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int i = e * 32 + lane, bx = i / HD;
-          page[e] = slot[e] = 0;
-          if (bx < nb && x.cached) {
-            pd.split(x.lo + bx * rows, page[e], slot[e]);
-            page[e] = P.table[(long long)g.b * P.ld_table + page[e]];
-            if (page[e] < 0 || page[e] >= P.num_pages) {
-              page[e] = 0;
-              bad_seg[seg & 15] = seg;
-            }
-          }
-        }
+      for (int kv = 0; kv < 2; ++kv) {
+        ok = ok && warp_wait(&empty[s], ph ^ 1);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
+        fills.note(s, ph);
         __syncwarp();
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int f = 2 * tc + kv, s = f % S::kSlots, ph = (f / S::kSlots) & 1;
-          ok = ok && warp_wait(&empty[s], ph ^ 1);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
-          fills.note(s, ph);
-          __syncwarp();
-          const uint32_t dst = smem_u32(ring + s * S::kSlot);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int i = e * 32 + lane, bx = i / HD, half = i % HD;
-            if (bx < nb) {
-              const uint32_t at = dst + half * S::kHalf + bx * rows * 128;
-              if (x.cached)
-                tma_4d(at, kv ? &maps.v : &maps.k, half * 64, slot[e], g.kvh, page[e], &full[s]);
-              else
-                tma_3d(at, kv ? &maps.vn : &maps.kn, half * 64, walk.r.cu + x.lo + bx * rows, g.kvh, &full[s]);
-            }
-          }
+        if (bx < nb) {
+          const uint32_t at = smem_u32(ring) + s * S::kSlot + half * S::kHalf + bx * rows * 128;
+          if (cur.x.cached)
+            tma_4d(at, kv ? &maps.v : &maps.k, half * 64, cur.slot, cur.kvh, cur.page, &full[s]);
+          else
+            tma_3d(at, kv ? &maps.vn : &maps.kn, half * 64, cur.row + bx * rows, cur.kvh, &full[s]);
+        }
+        if (++s == S::kSlots) {
+          s = 0;
+          ph ^= 1;
         }
       }
+      cur = next;
     }
     if (!ok) {
       dead = 1;

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import (SPEC_BF16, SPEC_OK, SpecError, _check_f32, _check_i32, _dtype_code, _ptr, _stream_handle, load_library)
+from . import SPEC_BF16, SPEC_OK, SpecError, _check_f32, _check_i32, _dtype_code, _ptr, load_library
 
 SPEC_F16 = 2
 SPEC_STATUS_BAD_PAGE = 32
@@ -126,6 +126,19 @@ def _raise(rc, where):
         raise SpecError(rc, where)
 
 
+def _stream_handle(stream) -> int:
+    """The stream's handle; the current one is asked for without building the
+    Python object around it, which costs more than a launch."""
+    import torch
+
+    if stream is not None:
+        return int(stream.cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return int(torch.cuda.current_stream().cuda_stream)
+    return raw(torch._C._cuda_getDevice())
+
+
 def _empty(stream, *shape, dtype, like):
     """A buffer on `like`'s device that belongs to the stream of the call."""
     import torch
@@ -146,7 +159,7 @@ def _check_out(name, t, shape, dtype):
     """A caller's buffer: contiguous, of this shape and type."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
 
 
@@ -166,7 +179,7 @@ def _check_vectors(name, t, dims, dtype):
 
 
 def _check_shape(name, t, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
