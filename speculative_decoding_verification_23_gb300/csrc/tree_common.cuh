@@ -66,6 +66,11 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& P, int b) {
   r.ct = (int)(((long long)r.ctx + P.kt - 1) / P.kt);
   r.per_item = r.ct + (r.n + P.kt - 1) / P.kt;
   r.mb = (r.n * P.group + P.rows - 1) / P.rows;
+  if (P.weigh) {
+    r.ok = r.ok && r.n <= r.ctx && r.ctx <= P.ld;
+    r.per_item = r.ct;
+    r.mb = 1;
+  }
   r.tiles = r.ok ? (long long)r.per_item * r.mb * P.heads : 0;
   return r;
 }

@@ -41,6 +41,9 @@ struct TreeParams {
   int grid;        // CTAs of the main kernel
   int rows;        // query rows per item
   int kt;          // keys per tile
+  int weigh;       // the rows are the last of the cached tokens: no drafted keys, all rows in one block,
+                   // and a request has at most `ld` tokens
+  int ld;
 };
 
 struct TreeWorkspace {

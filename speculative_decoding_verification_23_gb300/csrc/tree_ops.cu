@@ -19,6 +19,8 @@ bool tree_tc_fits(int dim, int page_size);
 TreePlan plan_tree_tc(int rows, int num_sms);
 int launch_tree_tc(const TreeParams& P, bool bf16, cudaStream_t s);
 int launch_tree_join(const TreeParams& P, bool bf16, int num_sms, cudaStream_t s);
+int weigh_tc_rows();
+int launch_weigh_tc(const TreeParams& P, const float* before, const float* lse, float* out, bool bf16, cudaStream_t s);
 int launch_weigh(const WeighParams& P, bool bf16, int num_sms, cudaStream_t s);
 int launch_evict(const EvictParams& P, cudaStream_t s);
 int launch_commit(const CommitParams& P, cudaStream_t s);
@@ -209,6 +211,42 @@ int spec_attention_weights(const spec_weigh_args* a, const float* before, float*
   int sms = 0;
   rc = sm_count(&sms);
   if (rc) return rc;
+  const bool bf16 = a->cache.dtype == SPEC_BF16;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const spec_cache& c = a->cache;
+  const long long rows = (long long)a->max_rows * (a->heads_q / c.heads);
+  if (sv::tree_tc_fits(c.dim, c.page_size) && rows <= sv::weigh_tc_rows() && tma_stride(c.s_slot, c.page_size) &&
+      tma_stride(c.s_head, c.heads) && tma_stride(c.s_page, c.num_pages)) {
+    sv::TreeParams P;
+    std::memset(&P, 0, sizeof(P));
+    P.cu = a->cu_rows;
+    P.ctx = a->kv_len;
+    P.table = a->block_table;
+    P.q = a->q;
+    P.k = layer_of(c.k, c, a->layer);
+    P.sq_node = a->sq_row;
+    P.sq_head = a->sq_head;
+    P.s_page = c.s_page;
+    P.s_slot = c.s_slot;
+    P.s_head = c.s_head;
+    P.status = out_status;
+    P.scale_log2 = a->scale * 1.4426950408889634f;
+    P.B = a->B;
+    P.total = a->total_rows;
+    P.max_nodes = a->max_rows;
+    P.ld_table = a->ld_table;
+    P.num_pages = c.num_pages;
+    P.page_size = c.page_size;
+    P.heads = c.heads;
+    P.group = a->heads_q / c.heads;
+    P.dim = c.dim;
+    P.grid = sms;
+    P.rows = 1;
+    P.kt = 128;
+    P.weigh = 1;
+    P.ld = a->ld;
+    return sv::launch_weigh_tc(P, before, a->lse, out, bf16, s) == 0 ? SPEC_OK : SPEC_ERR_LAUNCH;
+  }
   sv::WeighParams P;
   std::memset(&P, 0, sizeof(P));
   P.cu = a->cu_rows;
@@ -236,9 +274,7 @@ int spec_attention_weights(const spec_weigh_args* a, const float* before, float*
   P.heads = a->cache.heads;
   P.group = a->heads_q / a->cache.heads;
   P.dim = a->cache.dim;
-  return sv::launch_weigh(P, a->cache.dtype == SPEC_BF16, sms, reinterpret_cast<cudaStream_t>(stream)) == 0
-             ? SPEC_OK
-             : SPEC_ERR_LAUNCH;
+  return sv::launch_weigh(P, bf16, sms, s) == 0 ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 
 int spec_cache_evict(const spec_evict_args* a, int32_t* out_index, float* out_kept, int32_t* out_len,
