@@ -6,7 +6,9 @@ namespace sv {
 namespace {
 
 constexpr int kSelThreads = 1024;
-constexpr int kSelPer = 16;  // consecutive tokens per thread in the ordered pass
+constexpr int kSelPer = 16;  // consecutive tokens per thread
+constexpr int kSelHeld = kSelThreads * kSelPer;  // tokens whose keys stay in registers
+constexpr int kSelList = 96;                    // keys whose ranks are taken
 
 // A weight's order as an unsigned integer: larger is better, NaN the worst.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -15,103 +17,195 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ bool evict_bad_pages(const int32_t* row, long long tokens, int page_size, int num_pages) {
-  int bad = 0;
-  for (long long p = threadIdx.x; p < (tokens + page_size - 1) / page_size; p += blockDim.x) {
-    const int id = row[p];
-    bad |= id < 0 || id >= num_pages;
-  }
-  return __syncthreads_or(bad) != 0;
-}
-
-// One CTA per (request, head).  A radix select over the weights' order keys
-// (11, 11 and 10 bits) finds the key of the last kept token and how many of
-// its equals are kept; a pass in token order then writes the kept positions.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams P) {
+// Of tokens [lo, hi) of a longer row, the key of the need-th largest and how
+// many of its equals are kept: a radix select over the order keys (11, 11
+// and 10 bits), reading the weights three times.
+__device__ __noinline__ uint32_t select_long(const float* w, int lo, int hi, int* need_io) {
   __shared__ int hist[2048];
   __shared__ int warp_tot[kSelThreads / 32];
-  __shared__ unsigned long long warp_tot2[kSelThreads / 32];
   __shared__ int pick[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int need = *need_io, shift = 32;
+  uint32_t prefix = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int bits = pass < 2 ? 11 : 10;
+    const int above = shift;  // bits fixed: [above, 32)
+    shift -= bits;
+    for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int j = lo + tid; j < hi; j += kSelThreads) {
+      const uint32_t k = weight_key(w[j]);
+      if (above == 32 || (k >> above) == (prefix >> above)) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
+    }
+    __syncthreads();
+    // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t
+    const int x = hist[2047 - 2 * tid], y = hist[2046 - 2 * tid];
+    int v = x + y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += t;
+    }
+    if (lane == 31) warp_tot[warp] = v;
+    __syncthreads();
+    int base = 0;
+    for (int i = 0; i < warp; ++i) base += warp_tot[i];
+    const int incl = base + v, excl = incl - x - y;
+    if (excl < need && incl >= need) {  // one thread
+      const bool first = excl + x >= need;
+      pick[0] = first ? 2047 - 2 * tid : 2046 - 2 * tid;
+      pick[1] = need - (first ? excl : excl + x);
+    }
+    __syncthreads();
+    prefix |= (uint32_t)pick[0] << shift;
+    need = pick[1];
+    __syncthreads();
+  }
+  *need_io = need;
+  return prefix;
+}
+
+// One CTA per (request, head): the key of the last kept token and how many of
+// its equals are kept, then a pass in token order writes the kept positions.
+//
+// Rows of up to kSelHeld tokens are read once, their keys held in registers.
+// A key's bits are found one by one, by counts of the whole CTA, until few
+// keys are left between the bounds; these go to a list, where ranks decide.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams P) {
+  __shared__ int counts[2][kSelThreads / 32];
+  __shared__ uint32_t list[kSelList];
+  __shared__ int n_list, picked[2];
+  __shared__ unsigned long long warp_tot2[kSelThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int h = blockIdx.x % P.heads, b = blockIdx.x / P.heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int len = P.len[b];
   bool ok = len >= 0 && len <= P.ld && (long long)len <= (long long)P.ld_table * P.page_size;
   const int m = ok ? min(len, P.keep) : 0;
-  bool page_bad = false;
+  const float* w = P.weights + ((long long)b * P.heads + h) * P.ld;
+  const bool held = len <= kSelHeld;
+  const int lo = P.sink, hi = len - P.recent;  // chosen by weight: [lo, hi)
+  float x[kSelPer];
+#pragma unroll
+  for (int e = 0; e < kSelPer; ++e) x[e] = ok && held && tid * kSelPer + e < len ? w[tid * kSelPer + e] : 0.f;
+  int bad = 0;
   if (ok) {
-    page_bad = evict_bad_pages(P.table + (long long)b * P.ld_table, len, P.page_size, P.num_pages);
-    page_bad = evict_bad_pages(P.to + (long long)b * P.ld_to, m, P.page_size, P.num_pages) || page_bad;
+    // both tables' first entries at once: latency is what short rows cost
+    const int32_t* from_row = P.table + (long long)b * P.ld_table;
+    const int32_t* to_row = P.to + (long long)b * P.ld_to;
+    const int nf = len > 0 ? (len - 1) / P.page_size + 1 : 0, nt = m > 0 ? (m - 1) / P.page_size + 1 : 0;
+    const int f0 = tid < nf ? from_row[tid] : 0, t0 = tid < nt ? to_row[tid] : 0;
+    bad = f0 < 0 || f0 >= P.num_pages || t0 < 0 || t0 >= P.num_pages;
+    for (int p = tid + kSelThreads; p < nf; p += kSelThreads) bad |= from_row[p] < 0 || from_row[p] >= P.num_pages;
+    for (int p = tid + kSelThreads; p < nt; p += kSelThreads) bad |= to_row[p] < 0 || to_row[p] >= P.num_pages;
   }
+  bad = __syncthreads_or(bad);
   int32_t* index = P.index + ((long long)b * P.heads + h) * P.keep;
   float* kept = P.kept ? P.kept + ((long long)b * P.heads + h) * P.keep : nullptr;
   if (h == 0 && tid == 0) {
-    if (P.status) P.status[b] = !ok ? kStatusBadLen : (page_bad ? kStatusBadPage : 0);
-    P.new_len[b] = ok && !page_bad ? m : -1;
+    if (P.status) P.status[b] = !ok ? kStatusBadLen : (bad ? kStatusBadPage : 0);
+    P.new_len[b] = ok && !bad ? m : -1;
   }
-  ok = ok && !page_bad;
+  ok = ok && !bad;
   for (int i = (ok ? m : 0) + tid; i < P.keep; i += kSelThreads) {
     index[i] = -1;
     if (kept) kept[i] = 0.f;
   }
   if (!ok) return;
-  const float* w = P.weights + ((long long)b * P.heads + h) * P.ld;
   const bool all = len <= P.keep;
-  const int lo = P.sink, hi = len - P.recent;  // chosen by weight: [lo, hi)
-  int need = P.keep - P.sink - P.recent;       // of them (not for `all`)
-  uint32_t prefix = 0;                         // the last kept key so far
-  if (!all && need > 0) {
-    int shift = 32;
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int bits = pass < 2 ? 11 : 10;
-      const int above = shift;  // bits fixed: [above, 32)
-      shift -= bits;
-      for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int j = lo + tid; j < hi; j += kSelThreads) {
-        const uint32_t k = weight_key(w[j]);
-        if (above == 32 || (k >> above) == (prefix >> above)) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
-      }
-      __syncthreads();
-      // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t
-      const int x = hist[2047 - 2 * tid], y = hist[2046 - 2 * tid];
-      int v = x + y;
+  const int chosen = P.keep - P.sink - P.recent;
+  int need = chosen;     // of the tokens of key `prefix` (not for `all`)
+  uint32_t prefix = 0;   // the last kept key
+  bool from = false;     // all tokens of that key are kept, and all above it
+  uint32_t key[kSelPer];
+  if (held) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += t;
-      }
-      if (lane == 31) warp_tot[warp] = v;
-      __syncthreads();
-      int base = 0;
-      for (int i = 0; i < warp; ++i) base += warp_tot[i];
-      const int incl = base + v, excl = incl - x - y;
-      if (excl < need && incl >= need) {  // one thread
-        const bool first = excl + x >= need;
-        pick[0] = first ? 2047 - 2 * tid : 2046 - 2 * tid;
-        pick[1] = need - (first ? excl : excl + x);
-      }
-      __syncthreads();
-      prefix |= (uint32_t)pick[0] << shift;
-      need = pick[1];
-      __syncthreads();
+    for (int e = 0; e < kSelPer; ++e) {
+      const int j = tid * kSelPer + e;
+      key[e] = j >= lo && j < hi ? weight_key(x[e]) : 0u;  // 0 is NaN's: never probed
     }
   }
-  // `need` tokens of key `prefix` (the first ones) and all above it
+  if (!all && chosen > 0 && held) {
+    // `at` keys are at or above prefix, chosen <= at; `above` are at or above
+    // prefix + 2 bit, above < chosen
+    int above = 0, at = hi - lo, buf = 0;
+    const bool some = warp * 32 * kSelPer < len;  // this warp holds keys
+    if (tid == 0) n_list = 0;
+    int bit = 31;
+#pragma unroll 1
+    for (; bit >= 0 && at != chosen && at - above > kSelList; --bit) {
+      const uint32_t probe = prefix | (1u << bit);
+      int n = 0;
+      if (some) {
+#pragma unroll
+        for (int e = 0; e < kSelPer; ++e) n += key[e] >= probe;
+        n = __reduce_add_sync(0xffffffffu, n);
+      }
+      if (lane == 0) counts[buf][warp] = n;
+      __syncthreads();
+      n = __reduce_add_sync(0xffffffffu, counts[buf][lane]);
+      buf ^= 1;  // the other one was read before this barrier
+      if (n >= chosen) {
+        prefix = probe;
+        at = n;
+      } else {
+        above = n;
+      }
+    }
+    if (at == chosen) {
+      from = true;
+    } else if (bit < 0) {
+      need = chosen - above;  // more equals of one key than the list holds
+    } else {
+      // keys from prefix to below prefix + 2^(bit + 1), by rank
+      const uint32_t span = bit == 31 ? 0xffffffffu : (2u << bit) - 1u;
+      __syncthreads();
+      if (some) {
+#pragma unroll
+        for (int e = 0; e < kSelPer; ++e) {
+          const int j = tid * kSelPer + e;
+          if (j >= lo && j < hi && key[e] >= prefix && key[e] - prefix <= span) list[atomicAdd(&n_list, 1)] = key[e];
+        }
+      }
+      __syncthreads();
+      const int n = n_list, of = chosen - above;  // the of-th largest of the list
+      if (tid < n) {
+        const uint32_t k = list[tid];
+        int more = 0, same = 0;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+          more += list[i] > k;
+          same += list[i] == k;
+        }
+        if (more < of && more + same >= of) {  // one key, by all its equals alike
+          picked[0] = (int)k;
+          picked[1] = of - more;
+        }
+      }
+      __syncthreads();
+      prefix = (uint32_t)picked[0];
+      need = picked[1];
+    }
+  } else if (!all && chosen > 0) {
+    prefix = select_long(w, lo, hi, &need);
+  }
   unsigned long long done = 0;  // kept without ties, ties (32 bits each)
-  for (int base = 0; base < len; base += kSelThreads * kSelPer) {
+  for (int base = 0; base < len; base += kSelHeld) {
     const int j0 = base + tid * kSelPer;
     uint32_t sure = 0, tie = 0;
 #pragma unroll
     for (int e = 0; e < kSelPer; ++e) {
       const int j = j0 + e;
-      if (j >= len) break;
-      if (all || j < lo || j >= hi) {
-        sure |= 1u << e;
-      } else if (P.keep > P.sink + P.recent) {
-        const uint32_t k = weight_key(w[j]);
-        if (k > prefix) sure |= 1u << e;
-        if (k == prefix) tie |= 1u << e;
+      if (j < len) {
+        if (all || j < lo || j >= hi) {
+          sure |= 1u << e;
+        } else if (chosen > 0) {
+          if (!held) x[e] = w[j];
+          const uint32_t k = held ? key[e] : weight_key(x[e]);
+          if (k > prefix || (from && k == prefix)) sure |= 1u << e;
+          if (!from && k == prefix) tie |= 1u << e;
+        }
       }
     }
     unsigned long long v = ((unsigned long long)__popc(sure) << 32) | (unsigned)__popc(tie);
@@ -123,19 +217,22 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     }
     if (lane == 31) warp_tot2[warp] = v;
     __syncthreads();
-    unsigned long long at = done + v - mine, sum = 0;
-    for (int i = 0; i < kSelThreads / 32; ++i) {
-      if (i < warp) at += warp_tot2[i];
-      sum += warp_tot2[i];
+    unsigned long long before = lane < warp ? warp_tot2[lane] : 0ull, sum = warp_tot2[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
+    const unsigned long long at = done + before + v - mine;
     done += sum;
     int ns = (int)(at >> 32), nt = (int)(at & 0xffffffffu);
+#pragma unroll
     for (int e = 0; e < kSelPer; ++e) {
       const bool s = (sure >> e) & 1u, t = (tie >> e) & 1u;
       if (s || (t && nt < need)) {
         const int to = ns + min(nt, need);
         index[to] = j0 + e;
-        if (kept) kept[to] = w[j0 + e];
+        if (kept) kept[to] = held ? x[e] : w[j0 + e];
       }
       ns += s;
       nt += t;
@@ -151,6 +248,7 @@ constexpr int kMoveThreads = 256;
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams P, int blocks) {
   const int part = blockIdx.x % blocks, bh = blockIdx.x / blocks;
   const int h = bh % P.heads, b = bh / P.heads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the selection has ended
   const int m = P.new_len[b];
   const int pieces = P.dim / 8, per = kMoveThreads / pieces;
   const int i = part * per + (int)threadIdx.x / pieces, ch = threadIdx.x % pieces;
@@ -216,8 +314,20 @@ int launch_evict(const EvictParams& P, cudaStream_t s) {
   evict_select_kernel<<<P.B * P.heads, kSelThreads, 0, s>>>(P);
   if (cudaGetLastError() != cudaSuccess) return -1;
   const int per = kMoveThreads / (P.dim / 8), blocks = (P.keep + per - 1) / per;
-  evict_move_kernel<<<(unsigned)((long long)P.B * P.heads * blocks), kMoveThreads, 0, s>>>(P, blocks);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)P.B * P.heads * blocks));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;  // its launch runs beside the selection
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, evict_move_kernel, P, blocks) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  return 0;
 }
 
 int launch_commit(const CommitParams& P, cudaStream_t s) {
