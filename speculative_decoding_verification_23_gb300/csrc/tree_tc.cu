@@ -84,20 +84,21 @@ __device__ __noinline__ void add_odd(const TreeParams& P, int cu, int n, int nod
 // that copies tiles, and for each row tile one that issues its products.
 //
 // For every staged tile and each of the NT tiles of rows:
-//   S = Q K^T (both from shared memory), 128 keys in one go; then by 64 keys
-//   the softmax by the row's thread, P in 16 bits over the scores read, and
-//   O += P V (P from tensor memory), so that the product of one half runs
-//   during the softmax of the other.
-// With NT = 2 the two row tiles share a staged tile, and one's products run
-// during the other's softmax; with NT = 1 there are two score buffers, and
-// the next tile's scores are computed ahead.
+//   S = Q K^T (both from shared memory), by 64 keys the softmax by the row's
+//   thread, P in 16 bits over the scores read, O += P V (P from tensor
+//   memory), so that the products of one half run during the softmax of the
+//   other.
+// With NT = 1 there are two score buffers, and the next tile's scores are
+// computed ahead, 128 keys at once.  With NT = 2 the row tiles share a staged
+// tile, and each has one buffer: the next tile's scores take its halves one
+// by one.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     tree_tc_kernel(const TreeParams P, const __grid_constant__ TcMaps maps, int box) {
   using S = TcShape<D, NT>;
   constexpr int HD = D / 64;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t full[S::kSlots], empty[S::kSlots], q_full[NT], s_full[2], p_ready[4], o_half[NT], o_done[NT],
+  __shared__ uint64_t full[S::kSlots], empty[S::kSlots], q_full[NT], s_full[4], p_ready[4], o_half[NT], o_done[NT],
       o_last[NT], fin[NT], seg_end;
   __shared__ uint32_t tmem_at;
   // the last segments with a bad page (the copies run at most kSlots / 2
@@ -117,8 +118,10 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], NT);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&p_ready[i], 128);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_ready[i], 128);
+    }
     for (int i = 0; i < NT; ++i) {
       mbar_init(&q_full[i], 128);
       mbar_init(&o_half[i], 1);
@@ -240,30 +243,34 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
       r.n = uniform(walk.r.n);
       ok = warp_wait(&q_full[w], q_ph);
       q_ph ^= 1;
-      // scores of tile t
-      auto scores = [&](int t) {
-        const int buf = NT == 1 ? (t - t0) & 1 : w;
-        const uint32_t id = inst_desc<T>(tc_tile(r, t).n16, false);
-        const uint64_t db = dk + (uint32_t)(ks_ * (S::kSlot >> 4));
-        ok = ok && warp_wait(&full[ks_], k_ph);
+      // Scores of a tile: with one row tile, 128 keys at once into one of two
+      // buffers; with two, 64 keys (half h) as soon as the weights there have
+      // been used.
+      auto scores = [&](int t, int h) {
+        const int n16 = tc_tile(r, t).n16, buf = NT == 1 ? (t - t0) & 1 : w;
+        const uint32_t id = inst_desc<T>(NT == 1 ? n16 : min(kUnit, n16 - h * kUnit), false);
+        const uint64_t db = dk + (uint32_t)(ks_ * (S::kSlot >> 4) + h * ((kUnit * 128) >> 4));
+        if (h == 0) ok = ok && warp_wait(&full[ks_], k_ph);
         if (!ok) return;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = ((ks / 4) * S::kHalf + (ks % 4) * 32) >> 4;
-          mma_ss(tmem + buf * kTcKeys, da + off, db + off, id, ks > 0, one);
+          mma_ss(tmem + buf * kTcKeys + h * kUnit, da + off, db + off, id, ks > 0, one);
         }
-        mma_commit(&s_full[buf], one);
-        mma_commit(&empty[ks_], one);
-        ks_ += 2;
-        if (ks_ >= S::kSlots) {
-          ks_ -= S::kSlots;
-          k_ph ^= 1;
+        mma_commit(&s_full[buf * 2 + h], one);
+        if (NT == 1 || h == 1 || n16 <= kUnit) {
+          mma_commit(&empty[ks_], one);
+          ks_ += 2;
+          if (ks_ >= S::kSlots) {
+            ks_ -= S::kSlots;
+            k_ph ^= 1;
+          }
         }
       };
-      constexpr int AHEAD = 3 - NT;  // tiles whose scores are issued before the first product
-      scores(t0);
-      if (AHEAD > 1 && t0 + 1 < t1) scores(t0 + 1);
+      scores(t0, 0);
+      if (NT == 1 && t0 + 1 < t1) scores(t0 + 1, 0);
+      if (NT == 2 && tc_tile(r, t0).n16 > kUnit) scores(t0, 1);
       for (int t = t0; ok && t < t1; ++t) {
         const int n16 = tc_tile(r, t).n16, buf = NT == 1 ? (t - t0) & 1 : w;
         const uint64_t db = dv + (uint32_t)(vs_ * (S::kSlot >> 4));
@@ -279,9 +286,10 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
           for (int ks = 0; ks < n16 / 16; ++ks) mma_ts(o, p + ks * 8, db + ks * (2048 >> 4), id_v, ks > 0 || t > t0, one);
         }
         mma_commit(&o_half[w], one);
+        if (NT == 2 && t + 1 < t1) scores(t + 1, 0);
         p_ph ^= 1u << (buf * 2);
         if (n16 > kUnit) {
-          ok = warp_wait(&p_ready[buf * 2 + 1], (p_ph >> (buf * 2 + 1)) & 1);
+          ok = ok && warp_wait(&p_ready[buf * 2 + 1], (p_ph >> (buf * 2 + 1)) & 1);
           if (!ok) break;
           tc_fence_after();
           if (n16 == kTcKeys) {
@@ -294,7 +302,8 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
         }
         mma_commit(&o_done[w], one);  // before the scores that the softmax takes for a sign of it
         mma_commit(&empty[vs_], one);
-        if (t + AHEAD < t1) scores(t + AHEAD);
+        if (NT == 1 && t + 2 < t1) scores(t + 2, 0);
+        if (NT == 2 && t + 1 < t1 && tc_tile(r, t + 1).n16 > kUnit) scores(t + 1, 1);
         if (t == t1 - 1) mma_commit(&o_last[w], one);
         vs_ += 2;
         if (vs_ >= S::kSlots) {
@@ -402,12 +411,14 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         const int buf = NT == 1 ? (t - g.t0) & 1 : w;
-        ok = ok && warp_wait(&s_full[buf], (s_ph >> buf) & 1);
-        s_ph ^= 1u << buf;
-        if (!ok) break;
-        tc_fence_after();
 #pragma unroll 1
         for (int h = 0; h * kUnit < x.n16; ++h) {
+          if (NT == 2 || h == 0) {
+            ok = ok && warp_wait(&s_full[buf * 2 + h], (s_ph >> (buf * 2 + h)) & 1);
+            s_ph ^= 1u << (buf * 2 + h);
+            if (!ok) break;
+            tc_fence_after();
+          }
           const uint32_t s_at = tmem + lanes + buf * kTcKeys + h * kUnit;
           if (any) {
             float z[kUnit];
@@ -449,10 +460,10 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                 l3.y *= f;
               }
               if (t > g.t0 || h > 0) {
-                // The unit before is in O.  The scores of this tile came after
-                // the products of the tile two before (or one), so each of
-                // these barriers is at most one phase behind, which is all
-                // that a parity tells.
+                // The unit before is in O.  The scores here came after the
+                // products of the tile two before, and o_half follows o_done,
+                // so each of these barriers is at most one phase behind, which
+                // is all that a parity tells.
                 if (tc > 0) ok = warp_wait(&o_done[w], (tc - 1) & 1);
                 if (h > 0) ok = ok && warp_wait(&o_half[w], tc & 1);
                 if (!ok) break;
