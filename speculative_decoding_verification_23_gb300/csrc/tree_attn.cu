@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kWtWarps * 32, WtShape<D>::kCtas) tree_warp_ke
           P.lse[(long long)(r.cu + nd) * P.heads * P.group + head] = L == 0.f ? -INFINITY : (R + log2f(L)) * kLn2;
       } else {
         *reinterpret_cast<float2*>(P.part_o + (((long long)slot * (D / 4) + d / 4) * 16 + row) * 4 + d % 4) = make_float2(x, y);
-        if (d == 0) P.part_ml[(long long)slot * 16 + row] = make_float2(M, L);
+        if (d == 0) P.part_ml[(long long)slot * 16 + row] = make_float4(M, L, L, 0.f);
       }
     }
   }
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kJoinOf<D> * 32) tree_join_kernel(const TreePa
   const bool many = most > kJoinFew;
   const int step = many ? gridDim.y : gridDim.y * kJoinWarps;
   __shared__ float4 part[kJoinWarps][D / 16][32];
-  __shared__ float2 part_ml[kJoinWarps][8];
+  __shared__ float4 part_ml[kJoinWarps][8];
   for (int i = many ? blockIdx.y : blockIdx.y * kJoinWarps + warp; i < blocks * P.heads; i += step) {
     const int kvh = i / blocks, R0 = (i - kvh * blocks) * 8;
     const long long s = s0 + ((long long)kvh * r.mb + R0 / P.rows) * r.per_item;
@@ -360,20 +360,20 @@ __global__ void __launch_bounds__(kJoinOf<D> * 32) tree_join_kernel(const TreePa
     const int row = R0 % P.rows + (in ? sub : 0);
     // CTA c0 in slot 1, c0 + 1 .. c1 in slot 0; a running reference as in the
     // main kernel, four pieces' loads at once
-    float M = -INFINITY, L = 0.f;
+    float M = -INFINITY, L = 0.f, N = 0.f;  // N: the outputs' divisor
     float4 acc[D / 16];
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     const int by = many ? kJoinWarps : 1;
     constexpr int U = D <= 64 ? 4 : (D <= 128 ? 2 : 1);
     for (int c = c0 + (many ? warp : 0); c <= c1; c += U * by) {
-      float2 ml[U];
+      float4 ml[U];
       float4 v[U][D / 16];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int cu = c + u * by;
         const long long at = 2ll * cu + (cu == c0);
-        ml[u] = cu <= c1 ? __ldcg(&P.part_ml[at * P.rows + row]) : make_float2(-INFINITY, 0.f);
+        ml[u] = cu <= c1 ? __ldcg(&P.part_ml[at * P.rows + row]) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         const float4* src = reinterpret_cast<const float4*>(P.part_o) + (at * (D / 4) + quad) * P.rows + row;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(kJoinOf<D> * 32) tree_join_kernel(const TreePa
         const float to = fmaxf(M, ml[u].x), ref = to == -INFINITY ? 0.f : to;
         const float f = ex2(M - ref), h = ex2(ml[u].x - ref);
         L = L * f + ml[u].y * h;
+        N = N * f + ml[u].z * h;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           acc[k].x = acc[k].x * f + v[u][k].x * h;
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kJoinOf<D> * 32) tree_join_kernel(const TreePa
     }
     if (many) {
       __syncthreads();  // the last block's sums have been read
-      if (quad == 0) part_ml[warp][sub] = make_float2(M, L);
+      if (quad == 0) part_ml[warp][sub] = make_float4(M, L, N, 0.f);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) part[warp][k][lane] = acc[k];
       __syncthreads();
@@ -404,9 +405,13 @@ __global__ void __launch_bounds__(kJoinOf<D> * 32) tree_join_kernel(const TreePa
       M = -INFINITY;
       for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, part_ml[w][sub].x);
       const float ref = M == -INFINITY ? 0.f : M;
-      L = 0.f;
-      for (int w = 0; w < kJoinWarps; ++w) L += part_ml[w][sub].y * ex2(part_ml[w][sub].x - ref);
-      const float inv = L == 0.f ? 0.f : 1.f / L;
+      L = N = 0.f;
+      for (int w = 0; w < kJoinWarps; ++w) {
+        const float h = ex2(part_ml[w][sub].x - ref);
+        L += part_ml[w][sub].y * h;
+        N += part_ml[w][sub].z * h;
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / N;
       const int R = R0 + sub, node = in ? R / P.group : 0, head = kvh * P.group + (in ? R - node * P.group : 0);
       T* dst = out + (long long)(r.cu + node) * P.so_node + (long long)head * P.so_head + quad * 4;
       for (int k = warp; k < D / 16; k += kJoinWarps) {
@@ -433,7 +438,7 @@ __global__ void __launch_bounds__(kJoinOf<D> * 32) tree_join_kernel(const TreePa
     if (!in) continue;
     const float ref = M == -INFINITY ? 0.f : M;
     const int R = R0 + sub, node = R / P.group, head = kvh * P.group + R - node * P.group;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float inv = L == 0.f ? 0.f : 1.f / N;
     T* dst = out + (long long)(r.cu + node) * P.so_node + (long long)head * P.so_head + quad * 4;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {

@@ -32,7 +32,7 @@ struct TreeParams {
   float* lse;      // or null
   int32_t* status; // or null
   float* part_o;   // [2 * grid][dim / 4][rows][4] unnormalised outputs of split items
-  float2* part_ml; // [2 * grid][rows] their reference (log2 units) and sum
+  float4* part_ml; // [2 * grid][rows] their reference (log2 units), sum of weights, and of weights as rounded
   int32_t* failed; // [grid] whether a wait of a CTA ran out, or null
   long long* start;  // [B + 1] first tile of each request (main kernel to combine)
   float scale_log2;  // scale * log2(e)
@@ -57,7 +57,7 @@ inline TreeWorkspace make_tree_workspace(int B, int grid, int rows, int dim) {
   w.off_start = 0;
   w.off_failed = up256((size_t)(B + 1) * sizeof(long long));
   w.off_ml = w.off_failed + up256((size_t)grid * sizeof(int32_t));
-  w.off_o = w.off_ml + up256((size_t)2 * grid * rows * 2 * sizeof(float));
+  w.off_o = w.off_ml + up256((size_t)2 * grid * rows * 4 * sizeof(float));
   w.total = w.off_o + up256((size_t)2 * grid * rows * dim * sizeof(float));
   return w;
 }

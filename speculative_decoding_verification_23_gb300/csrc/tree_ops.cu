@@ -168,7 +168,7 @@ int spec_tree_attention(const spec_tree_args* a, void* out, int64_t so_node, int
   P.status = out_status;
   P.start = reinterpret_cast<long long*>(w + W.off_start);
   P.failed = plan.kernel == 1 ? reinterpret_cast<int32_t*>(w + W.off_failed) : nullptr;
-  P.part_ml = reinterpret_cast<float2*>(w + W.off_ml);
+  P.part_ml = reinterpret_cast<float4*>(w + W.off_ml);
   P.part_o = reinterpret_cast<float*>(w + W.off_o);
   P.scale_log2 = a->scale * 1.4426950408889634f;
   P.B = a->B;

@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
       const int node = mine ? (int)(((float)R + 0.5f) * inv_group) : 0;
       float m = -INFINITY;                 // the row's reference, log2 units
       float2 l2 = make_float2(0.f, 0.f), l3 = l2;  // its sum of 2^(s - m)
+      float fix = 0.f;                     // the rounding of the largest weights in it
       for (int t = g.t0; ok && t < g.t1; ++t, ++tc) {
         const TcTile x = tc_tile(r, t);
         uint32_t see[4];
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], z[e + 2 * k]), z[e + 2 * k + 1]);
             // the scale is positive
-            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * P.scale_log2;
+            const float zx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), mx = zx * P.scale_log2;
             // The reference follows the maximum only where it falls more than
             // 2^8 behind (or has none yet): weights up to 2^8 are exact in
             // fp32 sums and in range of both 16-bit types.
@@ -458,6 +459,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                 l2.y *= f;
                 l3.x *= f;
                 l3.y *= f;
+                fix *= f;
               }
               if (t > g.t0 || h > 0) {
                 // The unit before is in O.  The scores here came after the
@@ -481,6 +483,13 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
             }
             const float ref = m == -INFINITY ? 0.f : m;
             const float2 sc = make_float2(P.scale_log2, P.scale_log2), nr = make_float2(-ref, -ref);
+            // Where one key takes most of a row, the rounding of its weight
+            // for the product is the row's error (with the reference at the
+            // maximum it is 1, and exact).  So outputs are divided by a sum
+            // that holds each unit's largest weight as rounded; the others'
+            // roundings average out.
+            const float px = ex2(fmaf(zx, P.scale_log2, -ref));
+            fix += half_to_f32<T>(pack2<T>(px, 0.f) & 0xffffu) - px;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               uint32_t p[16];
@@ -520,7 +529,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
       const int slot = 2 * blockIdx.x + tree_slot(g.t0 == 0);
       float l = (l2.x + l2.y) + (l3.x + l3.y);
       if (poison) l = NAN;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float inv = l == 0.f ? 0.f : 1.f / (l + fix);
       const int head = g.kvh * P.group + R - node * P.group;
       T* dst = static_cast<T*>(P.out) + (long long)(r.cu + node) * P.so_node + (long long)head * P.so_head;
       const long long prow = (long long)slot * P.rows + w * kTcRows + row;
@@ -554,7 +563,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                         min(walk.r.n, (g.t1 - walk.r.ct) * kTcKeys), whole ? dst : nullptr, part);
         const float ref = m == -INFINITY ? 0.f : m;
         if (!whole)
-          P.part_ml[prow] = make_float2(m, l);
+          P.part_ml[prow] = make_float4(m, l, l + fix, 0.f);
         else if (P.lse)
           P.lse[(long long)(r.cu + node) * P.heads * P.group + head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
       }
