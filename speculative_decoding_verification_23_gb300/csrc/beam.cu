@@ -170,7 +170,7 @@ __device__ __forceinline__ bool beam_read(const BeamParams& P, int row) {
 
 struct BeamShared {
   float w_ref[kBmWarps], w_sum[kBmWarps], w_top[kBmWarps];
-  int w_cnt[kBmWarps];
+  int w_cnt[kBmWarps], w_cnt2[2][kBmWarps];
   float t_max[kBmThreads];
   int is_last, bad, n_got, n_hot, over;
   int place[kBeamMax];                       // of each row of the request in the split, -1: not read
@@ -302,9 +302,78 @@ struct BeamPool {
   int* hot;   // chunks
 };
 
-// The best K of the pool's n candidates, in order, to sh.best; the others go.
+// Leaves the best K of the pool's n > K candidates, in any order: bisections
+// over the scores' order keys and, among equals of the K-th, over places.
+__device__ __noinline__ void beam_cut(BeamShared& sh, BeamPool pool, int n, int K) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int PER = kBmCap / kBmThreads;
+  unsigned long long key[PER];
+  int flat[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int x = i * kBmThreads + tid;
+    key[i] = x < n ? pool.key[x] : 0ull;  // below every score's
+    flat[i] = x < n ? pool.flat[x] : 0x7fffffff;
+  }
+  int buf = 0;
+  auto total = [&](int v) {  // over the CTA
+    v = __reduce_add_sync(0xffffffffu, v);
+    if (lane == 0) sh.w_cnt2[buf][warp] = v;
+    __syncthreads();
+    v = __reduce_add_sync(0xffffffffu, lane < kBmWarps ? sh.w_cnt2[buf][lane] : 0);
+    buf ^= 1;
+    return v;
+  };
+  unsigned long long t = 0ull;  // the K-th best key
+  int at = n;
+#pragma unroll 1
+  for (int bit = 63; bit >= 0 && at != K; --bit) {
+    const unsigned long long probe = t | (1ull << bit);
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c += key[i] >= probe;
+    c = total(c);
+    if (c >= K) {
+      t = probe;
+      at = c;
+    }
+  }
+  int last = 0x7fffffff;  // the last place of an equal that stays
+  if (at != K) {
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c += key[i] > t;
+    const int need = K - total(c);
+    last = 0;
+#pragma unroll 1
+    for (int bit = 30; bit >= 0; --bit) {
+      const int probe = last | (1 << bit);
+      c = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c += key[i] == t && flat[i] < probe;
+      if (total(c) < need) last = probe;
+    }
+  }
+  if (tid == 0) sh.n_got = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (key[i] > t || (key[i] == t && key[i] != 0ull && flat[i] <= last)) {
+      const int to = atomicAdd(&sh.n_got, 1);
+      pool.key[to] = key[i];
+      pool.flat[to] = flat[i];
+    }
+  __syncthreads();
+}
+
+// The best K of the pool's n candidates, in order, to sh.best.
 __device__ __forceinline__ void beam_best(BeamShared& sh, const BeamPool& pool, int n, int K) {
-  for (int x = threadIdx.x; x < n; x += kBmThreads) {
+  if (n > kBmThreads) {
+    beam_cut(sh, pool, n, K);
+    n = K;
+  }
+  const int x = threadIdx.x;
+  if (x < n) {
     const unsigned long long k = pool.key[x];
     const int f = pool.flat[x];
     int rank = 0;
@@ -511,6 +580,30 @@ __device__ __forceinline__ void beam_finish(const BeamParams& P, BeamShared& sh,
       }
     }
   };
+  if (n_hot <= kBmHot && (n_chunk < 8 * K || n_hot > 2 * K + 16)) {
+    // Few chunks (a short vocabulary) bound the K-th best loosely or not at
+    // all: the same by threads' maxima over the tokens of these chunks.
+    best = -INFINITY;
+#pragma unroll 1
+    for (int i = warp; i < n_hot * kBmUnroll; i += kBmWarps) {
+      const int id = pool.hot[i / kBmUnroll], w = row_of(id);
+      const int tok = (id - w * P.chunks) * S::kChunk + (i % kBmUnroll * 32 + lane) * N;
+      float z[N];
+      cvt16(load_tail<T>(logits + (long long)w * P.ld, tok, P.V), z);
+      float top = z[0];
+#pragma unroll
+      for (int e = 1; e < N; ++e) top = fmaxf(top, z[e]);
+      if (top > -INFINITY) best = fmaxf(best, (top + sh.add[w]) - (sh.err[w] + 2.4e-7f * fabsf(top)));
+    }
+    sh.t_max[tid] = best;
+    __syncthreads();
+    const float floor2 = kth_bound(sh.t_max, K, lane);
+    for (int w = tid; w < P.W; w += kBmThreads) {
+      const float z = floor2 - sh.add[w];
+      sh.z_min[w] = fmaxf(sh.z_min[w], z - (sh.err[w] + 4.8e-7f * (fabsf(z) + fabsf(floor2))));
+    }
+    __syncthreads();
+  }
   if (n_hot <= kBmHot) {
     uint4 ahead[kBmUnroll];
     int w_next = 0, tok_next = 0;
@@ -548,34 +641,51 @@ __device__ __forceinline__ void beam_finish(const BeamParams& P, BeamShared& sh,
     // Too many at the bound (long runs of equal logits): chunk by chunk in
     // order, with the K-th best so far as the bound, ties by place.
     __syncthreads();
-    if (tid == 0) sh.n_got = n_ended;
+    if (tid == 0) {
+      sh.n_got = n_ended;
+      sh.over = 0;
+    }
     __syncthreads();
-    if (tid == 0) sh.over = 0;
+    n = n_ended;
+    // whether a chunk may hold a token that beats the bound
+    auto may = [&](int id, float m) {
+      const int w = row_of(id);
+      if (!(m > -INFINITY && m >= sh.z_min[w])) return false;
+      const unsigned long long k = double_key((double)sh.s0[w] + ((double)m - sh.lse[w]));
+      return k > tk || (k == tk && w * P.V + (id - w * P.chunks) * S::kChunk <= tf);
+    };
 #pragma unroll 1
-    for (int id = 0; id < n_chunk; ++id) {
-      const int row = row_of(id);
-      if (sh.place[row] < 0) continue;
-      const float m = __ldcg(maxima + id);
-      if (!(m > -INFINITY && m >= sh.z_min[row])) continue;
-      if (warp < kBmUnroll) {  // at most kBmCap - kChunk candidates before
-        const int tok = (id - row * P.chunks) * S::kChunk + (warp * 32 + lane) * N;
-        add_vector(row, tok, load_tail<T>(logits + (long long)row * P.ld, tok, P.V));
-      }
-      __syncthreads();
-      n = sh.n_got;
-      __syncthreads();
-      if (n > kBmCap - S::kChunk) {
-        beam_best(sh, pool, n, K);
-        for (int i = tid; i < K; i += kBmThreads) {
-          pool.key[i] = sh.best_key[i];
-          pool.flat[i] = sh.best_flat[i];
+    for (int base = 0; base < n_chunk; base += kBmThreads) {
+      const int mine = base + tid;
+      const float m = mine < n_chunk && sh.place[row_of(mine)] >= 0 ? __ldcg(maxima + mine) : -INFINITY;
+      const bool go = m > -INFINITY && may(mine, m);
+      sh.t_max[tid] = go ? m : -INFINITY;
+      if (__syncthreads_count(go) == 0) continue;
+#pragma unroll 1
+      for (int i = 0; i < kBmThreads; ++i) {
+        if (sh.t_max[i] == -INFINITY || !may(base + i, sh.t_max[i])) continue;  // the same for all threads
+        const int id = base + i, w = row_of(id);
+        if (warp < kBmUnroll) {  // at most kBmCap - kChunk candidates before
+          const int tok = (id - w * P.chunks) * S::kChunk + (warp * 32 + lane) * N;
+          add_vector(w, tok, load_tail<T>(logits + (long long)w * P.ld, tok, P.V));
         }
-        tk = sh.best_key[K - 1];
-        tf = sh.best_flat[K - 1];
-        if (tid == 0) sh.n_got = K;
         __syncthreads();
-        n = K;
+        n = sh.n_got;
+        __syncthreads();
+        if (n > kBmCap - S::kChunk) {
+          beam_best(sh, pool, n, K);
+          for (int x = tid; x < K; x += kBmThreads) {
+            pool.key[x] = sh.best_key[x];
+            pool.flat[x] = sh.best_flat[x];
+          }
+          tk = sh.best_key[K - 1];
+          tf = sh.best_flat[K - 1];
+          if (tid == 0) sh.n_got = K;
+          __syncthreads();
+          n = K;
+        }
       }
+      __syncthreads();
     }
   }
   beam_best(sh, pool, n, K);

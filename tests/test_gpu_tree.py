@@ -561,6 +561,20 @@ def test_beam_ties_go_to_the_lowest(dtype):
     check_beams(z, V, torch.tensor([[0.0, -1.5, -0.25], [0.0, -3.0, -0.5]], device="cuda"), 40)
 
 
+@pytest.mark.parametrize("W,keep,V", [(7, 18, 2075), (2, 64, 300), (1, 64, 70), (3, 33, 9001), (8, 64, 152064)])
+@pytest.mark.parametrize("allowed", [3, 40, 5000])
+def test_constrained_vocabularies(W, keep, V, allowed):
+    """Most tokens masked by the lowest finite value, fewer allowed than are kept, or not by much."""
+    for dtype in (torch.float32, torch.bfloat16):
+        g = torch.Generator(device="cuda").manual_seed(V + allowed)
+        z = torch.full((2 * W, V + (-V) % 8), torch.finfo(dtype).min, dtype=dtype, device="cuda")
+        at = torch.randperm(V, generator=g, device="cuda")[:allowed]
+        z[:, at] = (2 * torch.randn(2 * W, len(at), generator=g, device="cuda")).to(dtype)
+        check_beams(z, V, -2 * torch.rand(2, W, generator=g, device="cuda"), keep)
+        z[z == torch.finfo(dtype).min] = float("-inf")
+        check_beams(z, V, -2 * torch.rand(2, W, generator=g, device="cuda"), keep)
+
+
 def test_masked_logits_and_dead_beams():
     V, inf = 5000, float("inf")
     g = torch.Generator(device="cuda").manual_seed(4)
