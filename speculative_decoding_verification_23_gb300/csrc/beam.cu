@@ -2,6 +2,7 @@
 // new order.
 #include "stream_common.cuh"
 #include "tree_internal.h"
+#include "tree_launch.cuh"
 
 namespace sv {
 namespace {
@@ -706,6 +707,7 @@ __global__ void __launch_bounds__(kBmThreads, kBmCtas) beam_select_kernel(const 
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ BeamShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = P.B * P.W;
+  after_previous();
   BeamSplit sp;
   sp.steps = (P.V + S::kStep - 1) / S::kStep;
   if (R <= kBeamRows) {
@@ -826,6 +828,7 @@ __device__ __forceinline__ void copy_units(unsigned char* dst, const unsigned ch
 }
 
 __global__ void __launch_bounds__(kRoThreads) beam_reorder_kernel(const ReorderParams P) {
+  after_previous();
   int k = 0;
   while (k + 1 < P.num && (long long)blockIdx.x >= P.s[k + 1].first) ++k;
   const BeamState& s = P.s[k];
@@ -868,11 +871,8 @@ int launch_beam_select(const BeamParams& P, bool bf16, cudaStream_t s) {
   // the last CTA's candidates and chunks, then the rows that are read
   const long long rows = (long long)P.B * P.W;
   const int bytes = kBmCap * 12 + kBmHot * 4 + (rows <= kBeamRows ? (int)rows * 4 : 0);
-  if (bf16)
-    beam_select_kernel<__nv_bfloat16><<<P.grid, kBmThreads, bytes, s>>>(P);
-  else
-    beam_select_kernel<float><<<P.grid, kBmThreads, bytes, s>>>(P);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return bf16 ? launch_kernel(beam_select_kernel<__nv_bfloat16>, dim3(P.grid), kBmThreads, bytes, s, P)
+              : launch_kernel(beam_select_kernel<float>, dim3(P.grid), kBmThreads, bytes, s, P);
 }
 
 // Fills the work split of P's states and returns the number of blocks.
@@ -889,8 +889,7 @@ long long plan_reorder(ReorderParams& P) {
 }
 
 int launch_beam_reorder(const ReorderParams& P, long long blocks, cudaStream_t s) {
-  beam_reorder_kernel<<<(unsigned)blocks, kRoThreads, 0, s>>>(P);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return launch_kernel(beam_reorder_kernel, dim3((unsigned)blocks), kRoThreads, 0, s, P);
 }
 
 }  // namespace sv

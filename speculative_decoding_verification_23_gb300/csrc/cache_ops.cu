@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   __shared__ uint32_t list[kSelList];
   __shared__ int n_list, picked[2];
   __shared__ unsigned long long warp_tot2[kSelThreads / 32];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  after_previous();
   const int h = blockIdx.x % P.heads, b = blockIdx.x / P.heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int len = P.len[b];
@@ -248,7 +248,7 @@ constexpr int kMoveThreads = 256;
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams P, int blocks) {
   const int part = blockIdx.x % blocks, bh = blockIdx.x / blocks;
   const int h = bh % P.heads, b = bh / P.heads;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the selection has ended
+  after_previous();
   const int m = P.new_len[b];
   const int pieces = P.dim / 8, per = kMoveThreads / pieces;
   const int i = part * per + (int)threadIdx.x / pieces, ch = threadIdx.x % pieces;
@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 
 // One CTA per (request, layer): checks the request, then copies its path.
 __global__ void __launch_bounds__(kMoveThreads) commit_kernel(const CommitParams P) {
+  after_previous();
   const int b = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x;
   const int cu = P.cu[b], n = P.cu[b + 1] - cu, m = P.path_len[b], ctx = P.ctx[b];
   bool ok = cu >= 0 && n >= 0 && (long long)cu + n <= P.total && m >= 0 && m <= P.ld_path && ctx >= 0 &&
@@ -285,54 +286,56 @@ __global__ void __launch_bounds__(kMoveThreads) commit_kernel(const CommitParams
       const int node = path[i], id = table[page];
       bad |= (node < 0 || node >= n ? 1 : 0) | (id < 0 || id >= P.num_pages ? 2 : 0);
     }
-  const bool bad_node = __syncthreads_or(bad & 1) != 0, bad_page = __syncthreads_or(bad & 2) != 0;
+  bool bad_node = false, bad_page = false;
+  if (__syncthreads_or(bad)) {
+    bad_node = __syncthreads_or(bad & 1) != 0;
+    bad_page = __syncthreads_or(bad & 2) != 0;
+  }
   if (layer == 0 && tid == 0) {
     const int st = (!ok || bad_node ? kStatusBadLen : 0) | (bad_page ? kStatusBadPage : 0);
     if (P.status) P.status[b] = st;
     P.new_len[b] = st ? -1 : ctx + m;
   }
   if (!ok || bad_node || bad_page) return;
-  const int pieces = P.dim / 8, per_tok = P.heads * pieces;
-  for (int x = tid; x < m * per_tok; x += kMoveThreads) {
-    const int i = x / per_tok, y = x - i * per_tok, h = y / pieces, ch = y - h * pieces;
-    int page, slot;
-    pd.split(ctx + i, page, slot);
-    const long long from = (long long)layer * P.sn_layer + (long long)(cu + path[i]) * P.sn_node +
-                           (long long)h * P.sn_head + ch * 8;
-    const long long to = (long long)layer * P.s_layer + (long long)table[page] * P.s_page +
-                         (long long)slot * P.s_slot + (long long)h * P.s_head + ch * 8;
-    const uint4 k = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.k_new) + from);
-    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.v_new) + from);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.k) + to) = k;
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.v) + to) = v;
+  // four pieces of keys and of values a thread in flight
+  const int pieces = P.dim / 8, per_tok = P.heads * pieces, all = m * per_tok;
+  constexpr int U = 4;
+  for (int x0 = tid; x0 < all; x0 += U * kMoveThreads) {
+    long long to[U];
+    uint4 k[U], v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int x = x0 + u * kMoveThreads;
+      if (x >= all) continue;
+      const int i = x / per_tok, y = x - i * per_tok, h = y / pieces, ch = y - h * pieces;
+      int page, slot;
+      pd.split(ctx + i, page, slot);
+      const long long from = (long long)layer * P.sn_layer + (long long)(cu + path[i]) * P.sn_node +
+                             (long long)h * P.sn_head + ch * 8;
+      to[u] = (long long)layer * P.s_layer + (long long)table[page] * P.s_page + (long long)slot * P.s_slot +
+              (long long)h * P.s_head + ch * 8;
+      k[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.k_new) + from);
+      v[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.v_new) + from);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (x0 + u * kMoveThreads >= all) continue;
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.k) + to[u]) = k[u];
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.v) + to[u]) = v[u];
+    }
   }
 }
 
 }  // namespace
 
 int launch_evict(const EvictParams& P, cudaStream_t s) {
-  evict_select_kernel<<<P.B * P.heads, kSelThreads, 0, s>>>(P);
-  if (cudaGetLastError() != cudaSuccess) return -1;
+  if (launch_kernel(evict_select_kernel, dim3(P.B * P.heads), kSelThreads, 0, s, P)) return -1;
   const int per = kMoveThreads / (P.dim / 8), blocks = (P.keep + per - 1) / per;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)P.B * P.heads * blocks));
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr;  // its launch runs beside the selection
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, evict_move_kernel, P, blocks) != cudaSuccess) {
-    cudaGetLastError();
-    return -1;
-  }
-  return 0;
+  return launch_kernel(evict_move_kernel, dim3((unsigned)((long long)P.B * P.heads * blocks)), kMoveThreads, 0, s, P, blocks);
 }
 
 int launch_commit(const CommitParams& P, cudaStream_t s) {
-  commit_kernel<<<dim3(P.B, P.layers), kMoveThreads, 0, s>>>(P);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return launch_kernel(commit_kernel, dim3(P.B, P.layers), kMoveThreads, 0, s, P);
 }
 
 }  // namespace sv

@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kWtWarps * 32, WtShape<D>::kCtas) tree_warp_ke
   const T* vn = static_cast<const T*>(P.v_new);
   const T* q = static_cast<const T*>(P.q);
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  after_previous();
   const TreeScan scan = tree_scan(P, lane);
   if (blockIdx.x == 0 && warp == 0) tree_store_starts(P, scan, lane);
   TreeWalk walk;
@@ -308,9 +308,9 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kJoinOf<D> * 32) tree_join_kernel(const TreeParams P) {
   constexpr int kJoinWarps = kJoinOf<D>;
   const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  after_previous();
   const TreeReq r = tree_request(P, b);
   const int heads_q = P.heads * P.group;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.y == 0 && P.status) {
     int bad = 0;
     if (r.ok && r.n > 0) {
@@ -460,8 +460,7 @@ int launch_warp(const TreeParams& P, cudaStream_t s) {
     cudaGetLastError();
     return -1;
   }
-  tree_warp_kernel<T, D><<<P.grid, kWtWarps * 32, S::kSmem, s>>>(P);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return launch_kernel(tree_warp_kernel<T, D>, dim3(P.grid), kWtWarps * 32, S::kSmem, s, P);
 }
 
 template <typename T>
@@ -494,24 +493,10 @@ int launch_tree_warp(const TreeParams& P, bool bf16, cudaStream_t s) {
 namespace {
 template <typename T, int D>
 int launch_join(const TreeParams& P, int num_sms, cudaStream_t s) {
-  // A CTA for every 8 rows of the largest request, up to six per SM in all;
-  // they start while the main kernel ends and wait for it there.
+  // A CTA for every 8 rows of the largest request, up to six per SM in all.
   const long long rows = (long long)P.max_nodes * P.group, want = (rows + 7) / 8 * P.heads;
   const long long most = (6ll * num_sms + P.B - 1) / P.B;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(P.B, (unsigned)max(1ll, min(want, most)));
-  cfg.blockDim = dim3(kJoinOf<D> * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D>, P) != cudaSuccess) {
-    cudaGetLastError();
-    return -1;
-  }
-  return 0;
+  return launch_kernel(tree_join_kernel<T, D>, dim3(P.B, (unsigned)max(1ll, min(want, most))), kJoinOf<D> * 32, 0, s, P);
 }
 
 template <typename T>

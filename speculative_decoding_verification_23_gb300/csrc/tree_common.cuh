@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "tree_internal.h"
+#include "tree_launch.cuh"
 
 namespace sv {
 namespace {

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     odd_seg[0] = odd_seg[1] = -1;
     dead = 0;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  after_previous();
   const TreeScan scan = tree_scan(P, lane);
   if (blockIdx.x == 0 && warp == 0) tree_store_starts(P, scan, lane);
   tc_fence_before();
@@ -588,8 +588,7 @@ int launch_tc(const TreeParams& P, const TcMaps& maps, int box, cudaStream_t s) 
     cudaGetLastError();
     return -1;
   }
-  tree_tc_kernel<T, D, NT><<<P.grid, S::kThreads, S::kSmem, s>>>(P, maps, box);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return launch_kernel(tree_tc_kernel<T, D, NT>, dim3(P.grid), S::kThreads, S::kSmem, s, P, maps, box);
 }
 
 template <typename T>

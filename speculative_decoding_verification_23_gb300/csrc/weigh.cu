@@ -19,6 +19,7 @@ __global__ void __launch_bounds__(kWgWarps * 32) weigh_kernel(const WeighParams 
   __shared__ __align__(16) T qs[kWgRows * PITCH];
   __shared__ float ls[kWgRows];
   __shared__ int last_seen[kWgRows];  // last key that a row sees
+  after_previous();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int h = bh % P.heads, b = bh / P.heads;
@@ -121,16 +122,15 @@ __global__ void __launch_bounds__(kWgWarps * 32) weigh_kernel(const WeighParams 
 template <typename T>
 int launch_dim(const WeighParams& P, cudaStream_t s) {
   const int tiles = (P.ld + kWgKeys - 1) / kWgKeys;
-  const unsigned grid = (unsigned)((long long)tiles * P.B * P.heads);
+  const dim3 grid((unsigned)((long long)tiles * P.B * P.heads));
   switch (P.dim) {
-    case 64: weigh_kernel<T, 64><<<grid, kWgWarps * 32, 0, s>>>(P, tiles); break;
-    case 96: weigh_kernel<T, 96><<<grid, kWgWarps * 32, 0, s>>>(P, tiles); break;
-    case 128: weigh_kernel<T, 128><<<grid, kWgWarps * 32, 0, s>>>(P, tiles); break;
-    case 192: weigh_kernel<T, 192><<<grid, kWgWarps * 32, 0, s>>>(P, tiles); break;
-    case 256: weigh_kernel<T, 256><<<grid, kWgWarps * 32, 0, s>>>(P, tiles); break;
+    case 64: return launch_kernel(weigh_kernel<T, 64>, grid, kWgWarps * 32, 0, s, P, tiles);
+    case 96: return launch_kernel(weigh_kernel<T, 96>, grid, kWgWarps * 32, 0, s, P, tiles);
+    case 128: return launch_kernel(weigh_kernel<T, 128>, grid, kWgWarps * 32, 0, s, P, tiles);
+    case 192: return launch_kernel(weigh_kernel<T, 192>, grid, kWgWarps * 32, 0, s, P, tiles);
+    case 256: return launch_kernel(weigh_kernel<T, 256>, grid, kWgWarps * 32, 0, s, P, tiles);
     default: return -1;
   }
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace

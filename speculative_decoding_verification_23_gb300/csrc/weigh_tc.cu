@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     fence_mbar_init();
     dead = 0;
   }
+  after_previous();
   const TreeScan scan = tree_scan(P, lane);
   tc_fence_before();
   __syncthreads();
@@ -314,8 +315,7 @@ int launch_tc(const TreeParams& P, const float* before, const float* lse, float*
     cudaGetLastError();
     return -1;
   }
-  weigh_tc_kernel<T, D, RB><<<P.grid, kWtThreads, S::kSmem, s>>>(P, before, lse, out, map, box);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return launch_kernel(weigh_tc_kernel<T, D, RB>, dim3(P.grid), kWtThreads, S::kSmem, s, P, before, lse, out, map, box);
 }
 
 template <typename T, int D>
