@@ -14,8 +14,9 @@ __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// `beside`: whether the launch may overlap; otherwise it follows in stream order.
 template <typename... P, typename... A>
-int launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+int launch_beside(bool beside, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -25,12 +26,17 @@ int launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cud
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = beside ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
     cudaGetLastError();
     return -1;
   }
   return 0;
+}
+
+template <typename... P, typename... A>
+int launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  return launch_beside(true, kernel, grid, threads, smem, s, args...);
 }
 
 }  // namespace
