@@ -64,9 +64,11 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& P, int b) {
   r.ctx = P.ctx[b];
   r.ok = r.cu >= 0 && hi <= P.total && r.n >= 0 && r.n <= P.max_nodes && r.ctx >= 0 &&
          (long long)r.ctx <= (long long)P.ld_table * P.page_size;
-  r.ct = (int)(((long long)r.ctx + P.kt - 1) / P.kt);
-  r.per_item = r.ct + (r.n + P.kt - 1) / P.kt;
-  r.mb = (r.n * P.group + P.rows - 1) / P.rows;
+  // unsigned and by shifts: every role of a CTA does this before it begins
+  const int kt_shift = 31 - __clz(P.kt);  // a power of two
+  r.ct = (int)(((uint32_t)r.ctx + (uint32_t)P.kt - 1u) >> kt_shift);
+  r.per_item = r.ct + (int)(((uint32_t)r.n + (uint32_t)P.kt - 1u) >> kt_shift);
+  r.mb = (int)((uint32_t)(r.n * P.group + P.rows - 1) / (uint32_t)P.rows);
   if (P.weigh) {
     r.ok = r.ok && r.n <= r.ctx && r.ctx <= P.ld;
     r.per_item = r.ct;
@@ -126,12 +128,17 @@ __device__ __forceinline__ void tree_store_starts(const TreeParams& P, const Tre
   if (lane == 0) P.start[P.B] = s.total;
 }
 
+// a / b, by 32-bit division (several times faster) where both fit.
+__device__ __forceinline__ long long div_fast(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // CTA c of the G in use takes tiles [c*T/G, (c+1)*T/G), at least one each; and
 // the CTA that holds tile x.
 __device__ __forceinline__ int tree_used(const TreeParams& P, long long T) { return (int)min((long long)P.grid, T); }
-__device__ __forceinline__ long long tree_range(long long c, long long T, int G) { return c * T / G; }
+__device__ __forceinline__ long long tree_range(long long c, long long T, int G) { return div_fast(c * T, G); }
 __device__ __forceinline__ int tree_owner(long long x, long long T, int G) {
-  return (int)(((x + 1) * G + T - 1) / T - 1);
+  return (int)div_fast((x + 1) * G + T - 1, T) - 1;
 }
 
 // A run of tiles of one item inside a CTA's range (of the walk's request).
@@ -163,7 +170,7 @@ struct TreeWalk {
       r = tree_request(P, ++b);
     }
     const long long off = x - first;
-    const int item = (int)(off / r.per_item);
+    const int item = (int)div_fast(off, r.per_item);
     g.b = b;
     g.t0 = (int)(off - (long long)item * r.per_item);
     g.t1 = (int)min((long long)r.per_item, g.t0 + (end - x));

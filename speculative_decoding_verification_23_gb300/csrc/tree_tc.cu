@@ -332,8 +332,8 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
       const int nrows = min(kTcRows, r.n * P.group - row_lo);  // may be <= 0
       // This tile's query rows, swizzled as TMA would: 8 rows of 128 bytes a
       // pattern.  A thread copies one 16-byte piece of every (1024 / D)-th
-      // row, with 8 loads in flight.
-      constexpr int STEP = 1024 / D, N = 8;
+      // row, all its loads in flight at once.
+      constexpr int STEP = 1024 / D, N = kTcRows / STEP;
       const int ch = wtid % (D / 8);
       const T* src = static_cast<const T*>(P.q) + (long long)r.cu * P.sq_node + ch * 8;
 #pragma unroll 1
