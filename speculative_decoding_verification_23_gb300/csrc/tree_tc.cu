@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     odd_seg[0] = odd_seg[1] = -1;
     dead = 0;
   }
+  if (warp == 4 * NT && lane < 4) prefetch_map(lane == 0 ? &maps.k : lane == 1 ? &maps.v : lane == 2 ? &maps.kn : &maps.vn);
   after_previous();
   const TreeScan scan = tree_scan(P, lane);
   if (blockIdx.x == 0 && warp == 0) tree_store_starts(P, scan, lane);

@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     fence_mbar_init();
     dead = 0;
   }
+  if (tid == 128) prefetch_map(&k_map);
   after_previous();
   const TreeScan scan = tree_scan(P, lane);
   tc_fence_before();
