@@ -67,8 +67,11 @@ int check_cache(const spec_cache& c, bool need_v) {
   return SPEC_OK;
 }
 
-// A table of ld pages a request covers positions that fit 32 bits.
-bool table_ok(int ld, int page_size) { return ld >= 1 && (long long)ld * page_size <= INT32_MAX; }
+// Positions of tokens, and the step past the last of them that a loop takes,
+// fit 32 bits.
+constexpr int kMaxTokens = INT32_MAX - 65535;
+bool table_ok(int ld, int page_size) { return ld >= 1 && (long long)ld * page_size <= kMaxTokens; }
+bool row_ok(int ld) { return ld >= 1 && ld <= kMaxTokens; }
 
 int check_tree(const spec_tree_args* a) {
   if (!a) return SPEC_ERR_NULL;
@@ -98,11 +101,13 @@ bool tma_stride(int64_t s, int64_t n) { return n == 1 || (s > 0 && s < (1ll << 3
 // The tensor-memory kernel takes the calls whose tiles TMA can copy, with a
 // positive scale, and more query rows per key head than one warp tile holds.
 constexpr int kWarpRows = 16;
+// Up to here the kernel finds a row's node in fp32.
+constexpr int kMaxTcRows = 1 << 20;
 
 sv::TreePlan plan_tree(const spec_tree_args* a, int num_sms) {
   const spec_cache& c = a->cache;
   const int rows = a->max_nodes * (a->heads_q / c.heads);
-  const bool fits = sv::tree_tc_fits(c.dim, c.page_size) && a->scale > 0.f && a->total_nodes > 0 &&
+  const bool fits = rows <= kMaxTcRows && sv::tree_tc_fits(c.dim, c.page_size) && a->scale > 0.f && a->total_nodes > 0 &&
                     tma_stride(c.s_slot, c.page_size) && tma_stride(c.s_head, c.heads) &&
                     tma_stride(c.s_page, c.num_pages) && tma_stride(a->sn_node, a->total_nodes) &&
                     tma_stride(a->sn_head, c.heads);
@@ -195,7 +200,7 @@ int spec_attention_weights(const spec_weigh_args* a, const float* before, float*
   if (!a) return SPEC_ERR_NULL;
   int rc = check_cache(a->cache, false);
   if (rc) return rc;
-  if (a->B < 1 || a->total_rows < 0 || a->max_rows < 0 || a->ld < 1) return SPEC_ERR_SHAPE;
+  if (a->B < 1 || a->total_rows < 0 || a->max_rows < 0 || !row_ok(a->ld)) return SPEC_ERR_SHAPE;
   if ((long long)a->total_rows > (long long)a->B * a->max_rows) return SPEC_ERR_SHAPE;
   if (a->heads_q < 1 || a->heads_q % a->cache.heads != 0) return SPEC_ERR_SHAPE;
   if ((long long)a->max_rows * a->heads_q > INT32_MAX || (long long)a->B * a->cache.heads > INT32_MAX)
@@ -283,7 +288,7 @@ int spec_cache_evict(const spec_evict_args* a, int32_t* out_index, float* out_ke
   if (!a) return SPEC_ERR_NULL;
   int rc = check_cache(a->cache, true);
   if (rc) return rc;
-  if (a->B < 1 || a->keep < 1 || a->sink < 0 || a->recent < 0 || a->ld < 1) return SPEC_ERR_SHAPE;
+  if (a->B < 1 || a->keep < 1 || a->sink < 0 || a->recent < 0 || !row_ok(a->ld)) return SPEC_ERR_SHAPE;
   if ((long long)a->sink + a->recent > a->keep) return SPEC_ERR_SHAPE;
   if (a->layer < 0 || a->layer >= a->cache.layers) return SPEC_ERR_SHAPE;
   if (!table_ok(a->ld_table, a->cache.page_size) || !table_ok(a->ld_to, a->cache.page_size)) return SPEC_ERR_SHAPE;
@@ -329,7 +334,7 @@ int spec_cache_commit(const spec_commit_args* a, int32_t* out_len, int32_t* out_
   int rc = check_cache(a->cache, true);
   if (rc) return rc;
   if (a->B < 1 || a->total_nodes < 0 || a->ld_path < 1 || a->cache.layers > 65535) return SPEC_ERR_SHAPE;
-  if ((long long)a->ld_path * a->cache.heads * (a->cache.dim / 8) > INT32_MAX) return SPEC_ERR_SHAPE;
+  if ((long long)a->ld_path * a->cache.heads * (a->cache.dim / 8) > kMaxTokens) return SPEC_ERR_SHAPE;
   if (!table_ok(a->ld_table, a->cache.page_size)) return SPEC_ERR_SHAPE;
   if (!a->cu_nodes || !a->path || !a->path_len || !a->block_table || !a->ctx_len || !out_len) return SPEC_ERR_NULL;
   if (a->total_nodes > 0) {

@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     const uint32_t o_at = tmem + lanes + 2 * kTcKeys + w * D;
     unsigned char* qs = smem + w * S::kQBytes;
     uint32_t s_ph = 0;  // a bit per buffer
-    // node of a row: exact, as rows are below 2^22 and half a row from a multiple
+    // node of a row: exact, as rows are at most 2^20 and half a row from a multiple
     const float inv_group = 1.f / (float)P.group;
     bool ok = true;
     for (int seg = 0; ok && walk.next(P, g); ++seg) {
