@@ -114,7 +114,8 @@ int spec_tree_attention(const spec_tree_args *args, void *out, int64_t so_node, 
 /* ----------------------------------------------------- attention weights
  * The rows are the last n_b = cu_rows[b+1] - cu_rows[b] tokens of a cache of
  * kv_len[b] tokens: row i sees keys j <= kv_len[b] - n_b + i.  With their
- * lse (as spec_tree_attention gave it; a row whose lse is +inf adds nothing),
+ * lse (as spec_tree_attention gave it; a row whose lse is infinite, -inf where
+ * it saw nothing, adds nothing),
  *
  *   out[b, h, j] = before[b, h, j] + sum over rows i and the query heads of
  *                  key head h of exp(scale * q_i . k_j - lse_i),

@@ -80,7 +80,7 @@ __device__ __forceinline__ uint4 load_tail(const T* z, int at, int hi) {
   for (int e = 0; e < N; ++e) x[e] = none;
   uint4 v = *reinterpret_cast<const uint4*>(x);
   if (at < hi) {
-    v = __ldg(reinterpret_cast<const uint4*>(z + at));
+    v = load16(z + at);
     if (at + N > hi) {
       *reinterpret_cast<uint4*>(x) = v;
 #pragma unroll
@@ -195,7 +195,7 @@ __device__ __forceinline__ void beam_fetch(const BeamParams& P, const BeamPiece&
   const T* z0 = static_cast<const T*>(P.logits) + (long long)p.row * P.ld;
   if (x + (kBmUnroll - 1) * 32 * N + N <= p.hi) {
 #pragma unroll
-    for (int u = 0; u < kBmUnroll; ++u) v[u] = __ldg(reinterpret_cast<const uint4*>(z0 + x + u * 32 * N));
+    for (int u = 0; u < kBmUnroll; ++u) v[u] = load16(z0 + x + u * 32 * N);
   } else {
 #pragma unroll 1
     for (int u = 0; u < kBmUnroll; ++u) {

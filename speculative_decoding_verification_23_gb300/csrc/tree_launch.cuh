@@ -4,14 +4,26 @@
 // memory, until all work before it has ended.
 #pragma once
 
+#include <cstdint>
 #include <cuda_runtime.h>
 
 namespace sv {
 namespace {
 
+__device__ __forceinline__ void start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void after_previous() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  start_next();
+  wait_previous();
+}
+
+// 16 bytes that no kernel writes during this one.  Volatile, so that the load
+// stays behind the wait, which a load that the compiler may take for invariant
+// need not.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
 }
 
 // `beside`: whether the launch may overlap; otherwise it follows in stream order.

@@ -136,12 +136,13 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     dead = 0;
   }
   if (warp == 4 * NT && lane < 4) prefetch_map(lane == 0 ? &maps.k : lane == 1 ? &maps.v : lane == 2 ? &maps.kn : &maps.vn);
-  after_previous();
+  wait_previous();
   const TreeScan scan = tree_scan(P, lane);
   if (blockIdx.x == 0 && warp == 0) tree_store_starts(P, scan, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  start_next();  // not before this CTA has its tensor memory, which a kernel after it may want too
   const uint32_t tmem = uniform(tmem_at);
   TreeWalk walk;
   walk.begin(P, lane, scan, blockIdx.x);
@@ -346,8 +347,8 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
           v[i] = make_uint4(0, 0, 0, 0);
           if (rr < nrows) {
             const int nd = (int)(((float)R + 0.5f) * inv_group);
-            v[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)nd * P.sq_node +
-                                                        (long long)(g.kvh * P.group + R - nd * P.group) * P.sq_head));
+            v[i] = load16(src + (long long)nd * P.sq_node +
+                          (long long)(g.kvh * P.group + R - nd * P.group) * P.sq_head);
           }
         }
 #pragma unroll

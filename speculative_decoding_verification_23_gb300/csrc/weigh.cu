@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kWgWarps * 32) weigh_kernel(const WeighParams 
       ls[tid] = in ? P.lse[(long long)(cu + R / P.group) * P.heads * P.group + h * P.group + R % P.group] *
                          1.4426950408889634f
                    : INFINITY;
-      last_seen[tid] = in ? len - n + R / P.group : -1;
+      // padding and rows of infinite lse see nothing
+      last_seen[tid] = in && fabsf(ls[tid]) != INFINITY ? len - n + R / P.group : -1;
     }
     __syncthreads();
 #pragma unroll
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kWgWarps * 32) weigh_kernel(const WeighParams 
         for (int e = 0; e < 4; ++e) {
           const int row = (nt + x) * 8 + (lane & 3) * 2 + (e & 1), j = lo + (lane >> 2) + 8 * (e >> 1);
           const float p = ex2(fmaf(s[x][e], P.scale_log2, -ls[row]));
-          w[e >> 1] += j <= last_seen[row] && ls[row] < INFINITY ? p : 0.f;
+          w[e >> 1] += j <= last_seen[row] ? p : 0.f;
         }
     }
   }

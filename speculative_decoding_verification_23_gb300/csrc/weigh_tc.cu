@@ -35,6 +35,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   __shared__ uint64_t full[S::kSlots], empty[S::kSlots], s_full[2], s_free[2], q_full, fin;
   __shared__ __align__(16) float lse2[RB * kWtRows];
   __shared__ int last_key[RB * kWtRows];
+  __shared__ bool gaps[RB * kWtRows / 32];  // some of 32 rows add nothing
   __shared__ uint32_t tmem_at;
   __shared__ volatile int dead;
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -60,11 +61,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     dead = 0;
   }
   if (tid == 128) prefetch_map(&k_map);
-  after_previous();
+  wait_previous();
   const TreeScan scan = tree_scan(P, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  start_next();  // not before this CTA has its tensor memory, which a kernel after it may want too
   const uint32_t tmem = uniform(tmem_at);
   TreeWalk walk;
   walk.begin(P, lane, scan, blockIdx.x);
@@ -193,8 +195,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           v[i] = make_uint4(0, 0, 0, 0);
           if (R < rows) {
             const int nd = (int)(((float)R + 0.5f) * inv_group);
-            v[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)nd * P.sq_node +
-                                                        (long long)(g.kvh * P.group + R - nd * P.group) * P.sq_head));
+            v[i] = load16(src + (long long)nd * P.sq_node +
+                          (long long)(g.kvh * P.group + R - nd * P.group) * P.sq_head);
           }
         }
 #pragma unroll
@@ -209,14 +211,16 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       for (int rb = 0; rb < RB; ++rb) {
         const int R = rb * kWtRows + tid;
         float x = INFINITY;
-        int last = -1;
+        int last = -1;  // padding and rows of infinite lse see nothing
         if (R < rows) {
           const int nd = (int)(((float)R + 0.5f) * inv_group);
           x = row_lse[(long long)(r.cu + nd) * P.heads * P.group + g.kvh * P.group + R - nd * P.group];
-          if (x < INFINITY) last = r.ctx - r.n + nd;
+          if (fabsf(x) != INFINITY) last = r.ctx - r.n + nd;
         }
         lse2[R] = x * 1.4426950408889634f;
         last_key[R] = last;
+        const bool gap = __any_sync(0xffffffffu, last < 0);
+        if (lane == 0) gaps[R / 32] = gap;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(&q_full);
@@ -252,12 +256,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const float4* l4 = reinterpret_cast<const float4*>(lse2 + rb * kWtRows + c);
             const float2 sc = make_float2(P.scale_log2, P.scale_log2);
             const int* last = last_key + rb * kWtRows + c;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
+            // four rows' weights; `pick`: only of the rows that see key j
+            auto four = [&](int e, bool pick) {
               const float4 l = l4[e / 4];
               float2 a = __ffma2_rn(make_float2(z[e], z[e + 1]), sc, make_float2(-l.x, -l.y));
               float2 b = __ffma2_rn(make_float2(z[e + 2], z[e + 3]), sc, make_float2(-l.z, -l.w));
-              if (late) {
+              if (pick) {
                 a.x = j <= last[e] ? a.x : -INFINITY;
                 a.y = j <= last[e + 1] ? a.y : -INFINITY;
                 b.x = j <= last[e + 2] ? b.x : -INFINITY;
@@ -265,6 +269,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
               }
               w = __fadd2_rn(w, make_float2(ex2(a.x), ex2(a.y)));
               w1 = __fadd2_rn(w1, make_float2(ex2(b.x), ex2(b.y)));
+            };
+            const int left = min(kWtRows, rows - rb * kWtRows) - c;
+            if (left >= 32 && !late && !gaps[(rb * kWtRows + c) / 32]) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) four(e, false);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                if (e < left) four(e, true);
             }
           }
           tc_fence_before();
