@@ -88,7 +88,26 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   const int lo = P.sink, hi = len - P.recent;  // chosen by weight: [lo, hi)
   float x[kSelPer];
 #pragma unroll
-  for (int e = 0; e < kSelPer; ++e) x[e] = ok && held && tid * kSelPer + e < len ? w[tid * kSelPer + e] : 0.f;
+  for (int e = 0; e < kSelPer; ++e) x[e] = 0.f;
+  if (ok && held) {
+    // by 16 bytes where rows start on 16 (a row's last vector may pass its
+    // length, not ld); by 4 a warp's loads touch every sector four times
+    if (((reinterpret_cast<uintptr_t>(P.weights) | ((uintptr_t)P.ld * 4)) & 15) == 0) {
+#pragma unroll
+      for (int e = 0; e < kSelPer; e += 4)
+        if (tid * kSelPer + e < len) {
+          const float4 v = *reinterpret_cast<const float4*>(w + tid * kSelPer + e);
+          x[e] = v.x;
+          x[e + 1] = v.y;
+          x[e + 2] = v.z;
+          x[e + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kSelPer; ++e)
+        if (tid * kSelPer + e < len) x[e] = w[tid * kSelPer + e];
+    }
+  }
   int bad = 0;
   if (ok) {
     // both tables' first entries at once: latency is what short rows cost
