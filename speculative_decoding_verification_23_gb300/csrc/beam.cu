@@ -9,8 +9,12 @@ namespace {
 
 constexpr int kBmThreads = 256;
 constexpr int kBmWarps = kBmThreads / 32;
-constexpr int kBmUnroll = 4;      // 16-byte loads of a lane in a chunk
-constexpr int kBmCtas = 3;        // per SM
+// 16-byte loads of a lane in a chunk, and CTAs per SM.  64 x 8 beams over
+// 152064 bf16 logits and one request of 4 over 151936, with reordering, us:
+//   loads 4: one CTA 63 and 14.3, two 49 and 15.2, three 53 and 15.5, four 56 and 16.4;
+//   two CTAs: 2 loads 57 and 15.1, 8 loads 54 and 16.5.
+constexpr int kBmUnroll = 4;
+constexpr int kBmCtas = 2;
 constexpr int kBmCap = 2048;      // candidates of a request in shared memory
 constexpr int kBmHot = 1024;      // chunks that may hold candidates
 constexpr int kBeamRows = 2048;   // rows up to which those that are read are counted
