@@ -8,7 +8,9 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelPer = 16;  // consecutive tokens per thread
 constexpr int kSelHeld = kSelThreads * kSelPer;  // tokens whose keys stay in registers
-constexpr int kSelList = 96;                    // keys whose ranks are taken
+// Keys whose ranks are taken.  32 / 96 / 256: a batch cut to 2000 tokens a head
+// 60.2 / 60.2 / 61.7 us, one request cut to 1024 17.8 / 17.4 / 16.9.
+constexpr int kSelList = 96;
 
 // A weight's order as an unsigned integer: larger is better, NaN the worst.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -72,6 +74,8 @@ __device__ __noinline__ uint32_t select_long(const float* w, int lo, int hi, int
 // Rows of up to kSelHeld tokens are read once, their keys held in registers.
 // A key's bits are found one by one, by counts of the whole CTA, until few
 // keys are left between the bounds; these go to a list, where ranks decide.
+// Barriers bound it, not bytes: 16 requests of 8 heads and up to 16384 tokens,
+// 128 CTAs, take 20 us for 5 MB.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams P) {
   __shared__ int counts[2][kSelThreads / 32];
   __shared__ uint32_t list[kSelList];
@@ -261,7 +265,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 }
 
 // The move: 16-byte pieces of key and value rows, one kept token of a head
-// per `pieces` lanes.
+// per `pieces` lanes.  Bytes bound it: 2000 kept tokens of 128 heads of 128
+// channels, 262 MB read and written, 41 us, 6.4 TB/s.  Threads per CTA, here
+// and for the path, 64 / 128 / 256 / 512: with the selection 82 / 59.0 / 59.9 /
+// 61.9 us, 64 requests' paths 19.4 / 17.3 / 16.9 / 20.5.
 constexpr int kMoveThreads = 256;
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams P, int blocks) {
@@ -288,6 +295,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 }
 
 // One CTA per (request, layer): checks the request, then copies its path.
+// Latency bounds it, lengths to table to rows: 64 requests' paths of up to 33
+// nodes in 28 layers of 4 heads of 128 channels, 89 MB read and written, 16.9
+// us, 5.3 TB/s; one request's path 5.4 us.
 __global__ void __launch_bounds__(kMoveThreads) commit_kernel(const CommitParams P) {
   after_previous();
   const int b = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x;

@@ -1,6 +1,6 @@
 // Launches of the drafted-tree kernels: a kernel's launch overlaps the end of
 // the one before it on the stream (programmatic dependent launch).  Every
-// kernel lets the next one start at once and waits, before it touches any
+// kernel lets the next one start early and waits itself, before it touches any
 // memory, until all work before it has ended.
 #pragma once
 
