@@ -211,7 +211,9 @@ int spec_cache_commit(const spec_commit_args *args, int32_t *out_len, int32_t *o
  * there are fewer (a score of -inf, logits of -inf), the rest has score
  * -inf, parent -1 and token -1.  Scores are compared in 64 bits (row sums of
  * fp32 exponentials) and rounded once.  A NaN or +inf logit or score gives
- * the request SPEC_STATUS_BAD_LOGITS, scores -inf, parents and tokens -1. */
+ * the request SPEC_STATUS_BAD_LOGITS, scores -inf, parents and tokens -1; a
+ * logit from 2.3e38 on, which leaves fp32 once scaled by log2(e), counts as
+ * +inf. */
 typedef struct {
   int32_t B;
   int32_t W;           /* beams, 1 .. SPEC_MAX_BEAMS                         */

@@ -709,7 +709,7 @@ __device__ __forceinline__ void beam_finish(const BeamParams& P, BeamShared& sh,
 // 64 x 8 beams over 152064 bf16 logits, 158 MB: the logits are read in about 30
 // us (loads, exponentials and their issue), the last requests' continuations
 // take 12 us after that, dependent trips to L2 by one CTA a request, and the
-// beams' states 5 us; 49 us in all.  4 beams of one request: 15 us, latency.
+// beams' states 5 us; 48 us in all.  4 beams of one request: 15 us, latency.
 template <typename T>
 __global__ void __launch_bounds__(kBmThreads, kBmCtas) beam_select_kernel(const BeamParams P) {
   using S = BmShape<T>;
@@ -836,6 +836,9 @@ __device__ __forceinline__ void copy_units(unsigned char* dst, const unsigned ch
   }
 }
 
+// Latency bounds it, parents to rows: 64 x 8 beams' 500 tokens and 3584 values,
+// 9.4 MB read and written, 5 us.  Its launch overlaps the selection's end (48.4
+// us for both, 49.4 in stream order; 4 beams 15.2, 16.5).
 __global__ void __launch_bounds__(kRoThreads) beam_reorder_kernel(const ReorderParams P) {
   after_previous();
   int k = 0;
@@ -897,11 +900,8 @@ long long plan_reorder(ReorderParams& P) {
   return at;
 }
 
-// A launch of many CTAs does not overlap the selection before it: waiting, they
-// take the places of the kernel after them (64 x 8 beams: 59 us, against 53 in
-// stream order); one of few does (4 beams: 16 us, against 18).
-int launch_beam_reorder(const ReorderParams& P, long long blocks, int num_sms, cudaStream_t s) {
-  return launch_beside(blocks <= num_sms, beam_reorder_kernel, dim3((unsigned)blocks), kRoThreads, 0, s, P);
+int launch_beam_reorder(const ReorderParams& P, long long blocks, cudaStream_t s) {
+  return launch_kernel(beam_reorder_kernel, dim3((unsigned)blocks), kRoThreads, 0, s, P);
 }
 
 }  // namespace sv

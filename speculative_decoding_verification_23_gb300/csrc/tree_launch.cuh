@@ -26,9 +26,8 @@ __device__ __forceinline__ uint4 load16(const void* p) {
   return v;
 }
 
-// `beside`: whether the launch may overlap; otherwise it follows in stream order.
 template <typename... P, typename... A>
-int launch_beside(bool beside, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+int launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -38,17 +37,12 @@ int launch_beside(bool beside, void (*kernel)(P...), dim3 grid, int threads, siz
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = beside ? 1 : 0;
+  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
     cudaGetLastError();
     return -1;
   }
   return 0;
-}
-
-template <typename... P, typename... A>
-int launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
-  return launch_beside(true, kernel, grid, threads, smem, s, args...);
 }
 
 }  // namespace

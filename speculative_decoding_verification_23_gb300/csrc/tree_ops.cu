@@ -27,7 +27,7 @@ int launch_commit(const CommitParams& P, cudaStream_t s);
 void plan_beams(BeamParams& P, bool bf16, int num_sms);
 int launch_beam_select(const BeamParams& P, bool bf16, cudaStream_t s);
 long long plan_reorder(ReorderParams& P);
-int launch_beam_reorder(const ReorderParams& P, long long blocks, int num_sms, cudaStream_t s);
+int launch_beam_reorder(const ReorderParams& P, long long blocks, cudaStream_t s);
 }  // namespace sv
 
 namespace {
@@ -527,7 +527,7 @@ int spec_beam_reorder(int32_t B, int32_t W, int32_t keep, const int32_t* parents
   const int rc = sm_count(&sms);
   if (rc) return rc;
   if (blocks == 0) return SPEC_OK;
-  return sv::launch_beam_reorder(P, blocks, sms, reinterpret_cast<cudaStream_t>(stream)) == 0 ? SPEC_OK : SPEC_ERR_LAUNCH;
+  return sv::launch_beam_reorder(P, blocks, reinterpret_cast<cudaStream_t>(stream)) == 0 ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 
 }  // extern "C"
