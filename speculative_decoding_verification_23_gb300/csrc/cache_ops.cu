@@ -9,7 +9,7 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelPer = 16;  // consecutive tokens per thread
 constexpr int kSelHeld = kSelThreads * kSelPer;  // tokens whose keys stay in registers
 // Keys whose ranks are taken.  32 / 96 / 256: a batch cut to 2000 tokens a head
-// 60.2 / 60.2 / 61.7 us, one request cut to 1024 17.8 / 17.4 / 16.9.
+// 60.2 / 60.2 / 61.7 us.
 constexpr int kSelList = 96;
 
 // A weight's order as an unsigned integer: larger is better, NaN the worst.
@@ -72,10 +72,12 @@ __device__ __noinline__ uint32_t select_long(const float* w, int lo, int hi, int
 // its equals are kept, then a pass in token order writes the kept positions.
 //
 // Rows of up to kSelHeld tokens are read once, their keys held in registers.
-// A key's bits are found one by one, by counts of the whole CTA, until few
+// A key's bits are found two by two, by counts of the whole CTA, until few
 // keys are left between the bounds; these go to a list, where ranks decide.
-// Barriers bound it, not bytes: 16 requests of 8 heads and up to 16384 tokens,
-// 128 CTAs, take 20 us for 5 MB.
+// Barriers and comparisons bound it, not bytes: 16 requests of 8 heads and up to
+// 16384 tokens, 128 CTAs, take 15 us for 5 MB.  Bit by bit, one request cut from
+// 4000 tokens takes 14.4 us with its move, two by two 13.4; of 16384 tokens both
+// take as long.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams P) {
   __shared__ int counts[2][kSelThreads / 32];
   __shared__ uint32_t list[kSelList];
@@ -151,38 +153,53 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   }
   if (!all && chosen > 0 && held) {
     // `at` keys are at or above prefix, chosen <= at; `above` are at or above
-    // prefix + 2 bit, above < chosen
+    // prefix + 2^left, above < chosen
     int above = 0, at = hi - lo, buf = 0;
     const bool some = warp * 32 * kSelPer < len;  // this warp holds keys
     if (tid == 0) n_list = 0;
-    int bit = 31;
+    int left = 32;  // low bits of the key not found yet
 #pragma unroll 1
-    for (; bit >= 0 && at != chosen && at - above > kSelList; --bit) {
-      const uint32_t probe = prefix | (1u << bit);
-      int n = 0;
+    while (left > 0 && at != chosen && at - above > kSelList) {
+      left -= 2;
+      const uint32_t p1 = prefix + (1u << left), p2 = prefix + (2u << left), p3 = prefix + (3u << left);
+      int n = 0;  // three counts: a warp's are at most 512
       if (some) {
 #pragma unroll
-        for (int e = 0; e < kSelPer; ++e) n += key[e] >= probe;
+        for (int e = 0; e < kSelPer; ++e) {
+          n += key[e] >= p1 ? 1 : 0;
+          n += key[e] >= p2 ? 1 << 10 : 0;
+          n += key[e] >= p3 ? 1 << 20 : 0;
+        }
         n = __reduce_add_sync(0xffffffffu, n);
       }
       if (lane == 0) counts[buf][warp] = n;
       __syncthreads();
-      n = __reduce_add_sync(0xffffffffu, counts[buf][lane]);
+      n = counts[buf][lane];
       buf ^= 1;  // the other one was read before this barrier
-      if (n >= chosen) {
-        prefix = probe;
-        at = n;
+      const int n12 = __reduce_add_sync(0xffffffffu, (n & 1023) | ((n & (1023 << 10)) << 6));
+      const int n1 = n12 & 0xffff, n2 = n12 >> 16, n3 = __reduce_add_sync(0xffffffffu, n >> 20);
+      if (n3 >= chosen) {
+        prefix = p3;
+        at = n3;
+      } else if (n2 >= chosen) {
+        prefix = p2;
+        at = n2;
+        above = n3;
+      } else if (n1 >= chosen) {
+        prefix = p1;
+        at = n1;
+        above = n2;
       } else {
-        above = n;
+        above = n1;
       }
     }
     if (at == chosen) {
       from = true;
-    } else if (bit < 0) {
+    } else if (left == 0) {
       need = chosen - above;  // more equals of one key than the list holds
     } else {
-      // keys from prefix to below prefix + 2^(bit + 1), by rank
-      const uint32_t span = bit == 31 ? 0xffffffffu : (2u << bit) - 1u;
+      // keys from prefix to below prefix + 2^left, by rank
+      const uint32_t span = left == 32 ? 0xffffffffu : (1u << left) - 1u;
       __syncthreads();
       if (some) {
 #pragma unroll
@@ -248,17 +265,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     }
     const unsigned long long at = done + before + v - mine;
     done += sum;
-    int ns = (int)(at >> 32), nt = (int)(at & 0xffffffffu);
-#pragma unroll
-    for (int e = 0; e < kSelPer; ++e) {
-      const bool s = (sure >> e) & 1u, t = (tie >> e) & 1u;
-      if (s || (t && nt < need)) {
-        const int to = ns + min(nt, need);
-        index[to] = j0 + e;
-        if (kept) kept[to] = held ? x[e] : w[j0 + e];
-      }
-      ns += s;
-      nt += t;
+    // of this thread's ties the first that are still needed
+    const int nt = (int)(at & 0xffffffffu), room = max(0, need - nt);
+    while (__popc(tie) > room) tie &= ~(0x80000000u >> __clz(tie));
+    int to = (int)(at >> 32) + min(nt, need);
+    for (uint32_t take = sure | tie; take; take &= take - 1, ++to) {
+      const int j = j0 + __ffs(take) - 1;
+      index[to] = j;
+      if (kept) kept[to] = w[j];
     }
     __syncthreads();
   }
