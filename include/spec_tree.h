@@ -78,7 +78,8 @@ typedef struct {
  * and lse -inf.  What a row does not see never reaches it, NaN and
  * infinities included.  Statistics and sums are fp32; the weights are rounded
  * to the cache's type for their product with the values (unnormalised, the
- * row's running maximum at most 2^8), the result once more.
+ * row's running maximum between 1 and 2^8; with SPEC_F16 weights below 2^-14
+ * round to multiples of 2^-24), the result once more.
  *
  * A request with a bad length or page gets its status, and NaN in its rows
  * of out and lse. */
