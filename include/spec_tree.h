@@ -211,7 +211,8 @@ int spec_cache_commit(const spec_commit_args *args, int32_t *out_len, int32_t *o
  * continuations of a request, best first, ties to the lowest w*V + v.  Where
  * there are fewer (a score of -inf, logits of -inf), the rest has score
  * -inf, parent -1 and token -1.  Scores are compared in 64 bits (row sums of
- * fp32 exponentials) and rounded once.  A NaN or +inf logit or score gives
+ * fp32 exponentials, within 2^-21 of the score), so beams whose scores are
+ * nearer than that may take either order, and rounded once.  A NaN or +inf logit or score gives
  * the request SPEC_STATUS_BAD_LOGITS, scores -inf, parents and tokens -1; a
  * logit from 2.3e38 on, which leaves fp32 once scaled by log2(e), counts as
  * +inf. */

@@ -236,9 +236,10 @@ __device__ __forceinline__ void beam_piece(const BeamParams& P, BeamShared& sh, 
     const uint32_t key = __reduce_max_sync(0xffffffffu, float_key(top));
     if (lane == 0) __stcg(maxima + first / S::kChunk, key_float(key));
     best = fmaxf(best, top);
-    // the reference moves at the first finite logit, and then only where
-    // terms would come near fp32's range
-    if (top * L > ref + 60.f) {
+    // The reference moves at the first finite logit, and then where a lane's
+    // maximum has passed it by more than 2^4: an exponent of up to 4 is rounded
+    // by 2^-23 at most, and the terms that matter by as little.
+    if (top * L > ref + 4.f) {
       const float to = ceilf(top * L), f = pow2_int(ref - to);
       sum *= f;
       low *= f;

@@ -36,3 +36,14 @@ def test_a_request_of_many_that_has_no_number():
     want[150] = sv.SPEC_STATUS_BAD_LOGITS
     assert st.tolist() == want
     assert torch.all(torch.isneginf(s[150])) and torch.all(p[150] == -1) and torch.all(t[150] == -1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_whose_maximum_comes_late(dtype):
+    """The sum of a row is as exact where it is one logit's that stands far above those before it."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    V = 49488
+    z = 12 * torch.randn(100, V, generator=g, device="cuda")
+    z[:50] = z[:50].sort(1).values                                   # ascending
+    z[50:60, V // 2:] += torch.linspace(5, 45, 10, device="cuda")[:, None]
+    check_beams(z.to(TYPES[dtype]), V, -torch.rand(4, 25, generator=g, device="cuda"), 5)
