@@ -332,13 +332,10 @@ def _weigh(s):
     return {"weights": torch.where((j[None, :] < s["len"][:, None])[:, None], w, 0.0)}
 
 
-def _put(cache, table, page, pos, ok, values, heads):
-    """cache[page of pos, slot of pos, head] = values where ok; the other places keep what they hold."""
-    at = (torch.gather(table, 1, (pos.flatten(1) // page).clamp(max=table.shape[1] - 1).long()).view(pos.shape) * page
-          + pos % page).long()
-    flat = cache.view(-1, *cache.shape[2:])
-    old = flat[at, heads]
-    flat[at, heads] = torch.where(ok[..., None], values, old)
+def _put(cache, table, page, pos, values, heads):
+    """cache[page of pos, slot of pos, head] = values.  Places that repeat a position repeat its values."""
+    at = torch.gather(table, 1, (pos.flatten(1) // page).long()).view(pos.shape) * page + pos % page
+    cache.view(-1, *cache.shape[2:])[at.long(), heads] = values
 
 
 def _evict(s):
@@ -357,24 +354,25 @@ def _evict(s):
     index = torch.where(ok, index, -1)
     src = index.clamp(min=0)
     kept = torch.where(ok, torch.gather(w, 2, src), 0.0)
+    # what is moved: places past the kept tokens repeat the last of them
+    to = i.minimum(new_len[:, None, None] - 1).expand(by.shape)
+    src = torch.gather(src, 2, to.long())
     heads = torch.arange(s["kv_heads"], device=DEV)[None, :, None].expand(by.shape)
     at = torch.gather(s["table"], 1, (src // page).flatten(1)).view(src.shape) * page + src % page
     for name in ("k", "v"):
         values = s[name].view(-1, *s[name].shape[2:])[at.long(), heads]
-        _put(s[name], s["to_table"], page, i.expand(by.shape), ok, values, heads)
+        _put(s[name], s["to_table"], page, to, values, heads)
     return {"index": index.int(), "kept": kept, "new_len": new_len, "k": s["k"][s["first"]:], "v": s["v"][s["first"]:]}
 
 
 def _commit(s):
-    i = torch.arange(s["nodes"], device=DEV)
-    ok = i[None, :] < s["path_len"][:, None]
-    at = (s["cu"][:-1, None] + s["path"].clamp(min=0)).long()
-    pos = s["ctx"][:, None] + i[None, :]
-    page = torch.gather(s["table"], 1, (pos // s["page"]).clamp(max=s["table"].shape[1] - 1).long())
-    to = (page * s["page"] + pos % s["page"]).long()
+    # places past a path's end repeat its last node: two places of one slot write the same
+    i = torch.arange(s["nodes"], device=DEV).minimum(s["path_len"][:, None] - 1)
+    at = (s["cu"][:-1, None] + torch.gather(s["path"], 1, i.long())).long()
+    pos = s["ctx"][:, None] + i
+    to = (torch.gather(s["table"], 1, (pos // s["page"]).long()) * s["page"] + pos % s["page"]).long()
     for name in ("k", "v"):
-        flat = s[name].flatten(1, 2)  # a view: layers, slots, heads, dim
-        flat[:, to] = torch.where(ok[..., None, None], s[name + "_new"][:, at], flat[:, to])
+        s[name].flatten(1, 2)[:, to] = s[name + "_new"][:, at]  # a view: layers, slots, heads, dim
     return {"k": s["k"], "v": s["v"], "new_len": s["ctx"] + s["path_len"]}
 
 
