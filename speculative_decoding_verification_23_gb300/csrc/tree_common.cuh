@@ -72,7 +72,7 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& P, int b) {
   if (P.weigh) {
     r.ok = r.ok && r.n <= r.ctx && r.ctx <= P.ld;
     r.per_item = r.ct;
-    r.mb = 1;
+    r.mb = r.n > 0 ? 1 : 0;  // a request without rows has no tiles
   }
   r.tiles = r.ok ? (long long)r.per_item * r.mb * P.heads : 0;
   return r;
@@ -82,13 +82,19 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& P, int b) {
 struct TreeScan {
   long long before, mine, total;
   int per;
+  bool idle;  // this lane has a request of cached tokens without rows
 };
 
 __device__ __forceinline__ TreeScan tree_scan(const TreeParams& P, int lane) {
   TreeScan s;
   s.per = (P.B + 31) / 32;
   s.mine = 0;
-  for (int b = lane * s.per; b < min(P.B, (lane + 1) * s.per); ++b) s.mine += tree_request(P, b).tiles;
+  s.idle = false;
+  for (int b = lane * s.per; b < min(P.B, (lane + 1) * s.per); ++b) {
+    const TreeReq r = tree_request(P, b);
+    s.mine += r.tiles;
+    s.idle = s.idle || (r.ok && r.n == 0 && r.ctx > 0);
+  }
   long long v = s.mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {

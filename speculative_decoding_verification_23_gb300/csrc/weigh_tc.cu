@@ -19,12 +19,53 @@ struct WeighShape {
   static constexpr int kSmem = RB * kQBytes + kSlots * kSlot + 1024;
 };
 
+// The weights of requests without rows, by 128 threads: those of before, or 0.
+// All their keys, kIdle at a time, over the CTAs in turn.  16 requests of 8
+// heads and 16384 tokens, every second one without rows, kIdle 4096 / 1024 /
+// 512: 100 / 89 / 90 us, 104 with rows in all.  Not inlined, the call costs the
+// batch of the comment below 1.5 us, whether made or not.
+constexpr int kIdle = 1024;
+__device__ __forceinline__ void weigh_idle(const TreeParams& P, const float* before, float* out, int tid) {
+  const PageDiv pd(P.page_size);
+  const int parts = (P.ld + kIdle - 1) / kIdle;
+  for (long long u = blockIdx.x; u < (long long)P.B * P.heads * parts; u += gridDim.x) {
+    const long long row = u / parts;
+    const int b = (int)(row / P.heads), lo = (int)(u - row * parts) * kIdle;
+    const TreeReq r = tree_request(P, b);
+    if (!r.ok || r.n > 0) continue;
+    const int hi = min(r.ctx, lo + kIdle);
+    const int32_t* table = P.table + (long long)b * P.ld_table;
+    for (int j0 = lo + tid; j0 < hi; j0 += 4 * 128) {
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = j0 + i * 128;
+        x[i] = 0.f;
+        if (j >= hi) continue;
+        int page, slot;
+        pd.split(j, page, slot);
+        const int id = table[page];
+        if (before) x[i] = before[row * P.ld + j];
+        if (id < 0 || id >= P.num_pages) x[i] = NAN;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (j0 + i * 128 < hi) out[row * P.ld + j0 + i * 128] = x[i];
+    }
+  }
+}
+
 // Every CTA has an even share of all tiles of 128 keys (of all key heads of
 // all requests), in order, and keeps a head's query rows, up to RB blocks of
 // 128, while its tiles last.  Per tile and block of rows
 //   S = K Q^T,  w_j += sum_r 2^(scale log2(e) s_jr - log2(e) lse_r),
 // with two score buffers in tensor memory.  Warps 0 - 3: one key a thread;
 // warp 4 copies key tiles, warp 5 issues products.
+//
+// Requests without rows have no tiles: the sums wait for the products by a
+// segment's scores alone, so with no scores they could complete q_full twice
+// while the products still wait for its first phase, and a parity does not
+// tell phases apart that are two away.
 //
 // A key's sum is one thread's, so there are no atomics and no second pass, and
 // nothing but the keys, read once, and a float per key moves: the copies bound
@@ -299,6 +340,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       asm volatile("bar.sync 1, 128;" ::: "memory");
       ok = ok && !dead;
     }
+    if (__any_sync(0xffffffffu, scan.idle)) weigh_idle(P, before, out, tid);
     // zeros past the lengths, NaN for bad requests, and the statuses
     for (long long i = blockIdx.x; i < (long long)P.B * P.heads; i += gridDim.x) {
       const int b = (int)(i / P.heads), h = (int)(i - (long long)b * P.heads);
