@@ -7,11 +7,22 @@
 
 #include <vector_types.h>
 
+struct CUstream_st;  // cudaStream_t is a pointer to it
+
 namespace sv {
 
 // Call-tagged arrival counters (tagged_arrive): bits of a counter word below
 // the call's tag, i.e. the most arrivals one call may count.
 constexpr int kTagShift = 24;
+
+// Tags of the calls whose kernels count arrivals in words of a workspace: one
+// per call, in [1, 2^40), from one count for all entry points, as any of them
+// may be given a workspace that another has used.  Outside stream capture a
+// call takes a fresh tag and enqueues nothing but its kernel.  Under capture
+// the tag would be replayed with the graph, so the call captures a clear of its
+// B counters instead and uses tag 0, which a cleared word carries.  Returns
+// SPEC_OK or a SPEC_ERR_*.
+int call_tag(unsigned long long* counters, int B, CUstream_st* s, unsigned long long* tag);
 
 // ----------------------------------------------------------------- sampling
 constexpr int kChunk = 256;                 // tokens per warp-chunk (8 per lane)

@@ -118,12 +118,11 @@ struct NvtxRange {
 constexpr long long kSegWaitLimit = 4000000000ll;
 std::atomic<long long> g_seg_wait_limit{kSegWaitLimit};
 
-// Tags of the calls whose kernels count arrivals with tagged_arrive: one per
-// call, in [1, 2^40).  Outside stream capture a call takes a fresh tag and
-// enqueues nothing but its kernel.  Under capture the tag would be replayed
-// with the graph, so the call captures a clear of its B counters instead and
-// uses tag 0, which a cleared word carries.
 std::atomic<unsigned long long> g_call_tag{0};
+
+}  // namespace
+
+namespace sv {
 
 int call_tag(unsigned long long* counters, int B, cudaStream_t s, unsigned long long* tag) {
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
@@ -139,10 +138,14 @@ int call_tag(unsigned long long* counters, int B, cudaStream_t s, unsigned long 
     *tag = 0;
     return SPEC_OK;
   }
-  const unsigned long long span = (1ull << (64 - sv::kTagShift)) - 1ull;
+  const unsigned long long span = (1ull << (64 - kTagShift)) - 1ull;
   *tag = g_call_tag.fetch_add(1, std::memory_order_relaxed) % span + 1ull;
   return SPEC_OK;
 }
+
+}  // namespace sv
+
+namespace {
 
 // The split-vocabulary kernel can serve sampling without top-p when a row
 // has at most kSegMaxSegs segments (V <= 491520 bf16, 245760 fp32).
@@ -273,7 +276,7 @@ int run_topp(const sv::SampleParams& S, const spec_args* a, void* ws, int num_sm
   P.broken = reinterpret_cast<unsigned long long*>(w + W.off_ctr);
   P.pool = reinterpret_cast<int*>(w + W.off_pool);
   P.pool_cap = W.pool_cap;
-  const int rc = call_tag(P.broken, 1, stream, &P.tag);
+  const int rc = sv::call_tag(P.broken, 1, stream, &P.tag);
   if (rc) return rc;
   return sv::launch_topp_verify(P, a->dtype == SPEC_BF16, num_sms, stream) == 0 ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
@@ -317,7 +320,7 @@ int run_sample(sv::SampleParams& P, const spec_args* a, void* ws, size_t ws_byte
   P.inval = reinterpret_cast<int*>(w + W.off_inval);
   P.tag = 0;
   if (P.mode == sv::kModeSample) {
-    rc = call_tag(P.counters, a->B, stream, &P.tag);
+    rc = sv::call_tag(P.counters, a->B, stream, &P.tag);
     if (rc) return rc;
   }
   if (!resident && pipe_ok) {
@@ -465,7 +468,7 @@ int spec_verify_greedy(const spec_args* a, int32_t* out_tokens, int32_t* out_acc
   P.out_status = out_status;
   P.counters = reinterpret_cast<unsigned long long*>(w + W.off_counters);
   P.partials = reinterpret_cast<sv::GreedyPartial*>(w + W.off_partials);
-  rc = call_tag(P.counters, a->B, s, &P.tag);
+  rc = sv::call_tag(P.counters, a->B, s, &P.tag);
   if (rc) return rc;
   return sv::launch_greedy_verify(P, a->dtype == SPEC_BF16, s) == 0 ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
@@ -515,7 +518,7 @@ int spec_draft_confidence(const spec_args* a, float threshold, float* out_conf, 
   P.out_status = out_status;
   P.counters = reinterpret_cast<unsigned long long*>(w + W.off_counters);
   P.partials = reinterpret_cast<sv::ConfPartial*>(w + W.off_partials);
-  rc = call_tag(P.counters, a->B, s, &P.tag);
+  rc = sv::call_tag(P.counters, a->B, s, &P.tag);
   if (rc) return rc;
   // at least one draft row per SM: the pipelined kernel (whole rows per
   // CTA); smaller batches spread each row over 8192-token chunks

@@ -1,6 +1,5 @@
 // C ABI of the drafted-tree operators: host-side checks, the choice of
 // kernel, launches.
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -418,29 +417,6 @@ void beam_params(sv::BeamParams& P, const spec_beam_args* a, int num_sms) {
   sv::plan_beams(P, a->dtype == SPEC_BF16, num_sms);
 }
 
-// Tags of the calls whose kernels count arrivals (see tagged_arrive), as in
-// spec_verify.cu; under stream capture the counters are cleared instead.
-std::atomic<unsigned long long> g_beam_tag{0};
-
-int beam_tag(unsigned long long* counters, int B, cudaStream_t s, unsigned long long* tag) {
-  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) {
-    cudaGetLastError();
-    return SPEC_ERR_LAUNCH;
-  }
-  if (cs != cudaStreamCaptureStatusNone) {
-    if (cudaMemsetAsync(counters, 0, (size_t)B * sizeof(unsigned long long), s) != cudaSuccess) {
-      cudaGetLastError();
-      return SPEC_ERR_LAUNCH;
-    }
-    *tag = 0;
-    return SPEC_OK;
-  }
-  const unsigned long long span = (1ull << (64 - sv::kTagShift)) - 1ull;
-  *tag = g_beam_tag.fetch_add(1, std::memory_order_relaxed) % span + 1ull;
-  return SPEC_OK;
-}
-
 }  // namespace
 
 extern "C" {
@@ -481,7 +457,7 @@ int spec_beam_select(const spec_beam_args* a, float* out_scores, int32_t* out_pa
   P.counters = reinterpret_cast<unsigned long long*>(w + W.off_counters);
   P.stat = reinterpret_cast<float4*>(w + W.off_stat);
   P.maxima = reinterpret_cast<float*>(w + W.off_maxima);
-  rc = beam_tag(P.counters, a->B, s, &P.tag);
+  rc = sv::call_tag(P.counters, a->B, s, &P.tag);
   if (rc) return rc;
   return sv::launch_beam_select(P, a->dtype == SPEC_BF16, s) == 0 ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
