@@ -82,7 +82,8 @@
  * and every call is one kernel launch: the split-vocabulary sampling kernel
  * clears its counters itself at its start; the other kernels count each
  * request's arrivals on a 64-bit word tagged with the call (a process-wide
- * call number in [1, 2^40)), and a word with another tag counts as zero.
+ * call number in [1, 2^40), counted from a number that other data's words
+ * seldom carry), and a word with another tag counts as zero.
  * Under stream capture the tag would replay with the graph, so a captured
  * call also captures a cudaMemsetAsync of its B counter words (tag 0).
  * Calls that share one workspace must be ordered (same stream, or

@@ -1,8 +1,7 @@
-"""One workspace for calls of every kind in turn.
+"""One workspace for calls of every kind in turn, and one that held other data.
 
-The calls run in a process of their own, so that each kind of call is as old
-as the others when they meet: the counters of a workspace tell calls apart by
-their numbers."""
+The calls run in a process of their own, so that their numbers, by which the
+counters of a workspace tell calls apart, begin anew."""
 import os
 import subprocess
 import sys
@@ -57,4 +56,51 @@ print("equal")
 @pytest.mark.parametrize("which", ["greedy", "confidence", "resident", "streaming"])
 def test_beams_and_a_verify_call_share_a_workspace(which):
     r = subprocess.run([sys.executable, "-c", PROGRAM, which], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "equal", (r.stdout + r.stderr)[-2000:]
+
+
+HELD = """
+import sys
+import torch
+import speculative_decoding_verification_23_gb300 as sv
+from speculative_decoding_verification_23_gb300 import workload as W
+from speculative_decoding_verification_23_gb300.device_batch import to_device
+
+if sys.argv[1] == "greedy":
+    batch = W.make_batch(B=5, V=20000, K=[0, 1, 3, 5, 2], dtype="bf16", seed=5, rho=0.9, temperature=0.7,
+                         rep_penalty=1.0, hist_len=4, top_p=1.0, tv_budget=0.2)
+    db = to_device(batch)
+    need = sv.spec_workspace_bytes(5, int(batch.cu_draft[-1]), 20000)
+    total = int(batch.cu_draft[-1]) + 5
+    outs = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (total, 5, 5)]
+    names = ("out_tokens", "out_accepted", "out_status")
+    run = lambda ws: sv.spec_verify_greedy(db.args(), workspace=ws, **dict(zip(names, outs)))
+else:
+    g = torch.Generator(device="cuda").manual_seed(1)
+    z = (3 * torch.randn(5 * 4, 20000, generator=g, device="cuda")).bfloat16()
+    a = sv.make_beam_args(logits=z, V=20000, scores=torch.zeros(5, 4, device="cuda"), keep=4)
+    need = sv.spec_beam_workspace_bytes(a)
+    outs = [torch.empty(5, 4, device="cuda"), *(torch.empty(5, 4, dtype=torch.int32, device="cuda") for _ in range(2)),
+            torch.empty(5, dtype=torch.int32, device="cuda")]
+    names = ("out_scores", "out_parents", "out_tokens", "out_status")
+    run = lambda ws: sv.spec_beam_select(a, workspace=ws, **dict(zip(names, outs)))
+def call(ws):
+    for x in outs:
+        x.fill_(-9)
+    return run(ws)
+want = [x.clone() for x in call(torch.zeros(need, dtype=torch.uint8, device="cuda"))]
+ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+words = ws[:need // 8 * 8].view(torch.int32).view(-1, 2)
+for n in range(2, 200):
+    words[:, 0] = (n << 24 | 0x8005) - (1 << 32 if n > 127 else 0)  # a float of exponent n, before a zero
+    words[:, 1] = 0
+    for x, y in zip(want, call(ws)):
+        assert torch.equal(x, y), n
+print("equal")
+"""
+
+
+@pytest.mark.parametrize("which", ["greedy", "beams"])
+def test_a_workspace_that_held_floats(which):
+    r = subprocess.run([sys.executable, "-c", HELD, which], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "equal", (r.stdout + r.stderr)[-2000:]
