@@ -157,8 +157,8 @@ int spec_attention_weights(const spec_weigh_args *args, const float *before, flo
  *
  * out_index [B, heads, keep]: the kept positions ascending, then -1;
  * out_kept [B, heads, keep] (may be NULL): their weights, then 0; out_len
- * [B] = m_b.  A request with a bad length or page gets its status and
- * out_len -1, index -1, kept 0, and nothing of it is moved. */
+ * [B] = m_b (may be kv_len itself).  A request with a bad length or page gets
+ * its status and out_len -1, index -1, kept 0, and nothing of it is moved. */
 typedef struct {
   int32_t B;
   int32_t keep;   /* >= sink + recent, >= 1                                  */
@@ -181,8 +181,9 @@ int spec_cache_evict(const spec_evict_args *args, int32_t *out_index, float *out
 /* ---------------------------------------------------- the accepted path
  * Writes node path[b, i] of request b (i < path_len[b] <= ld_path) to token
  * ctx_len[b] + i of every layer of the cache; out_len[b] = ctx_len[b] +
- * path_len[b].  A request with a bad length, a node outside its tree or a
- * bad page gets its status and out_len -1, and nothing of it is written. */
+ * path_len[b] (out_len may be ctx_len itself).  A request with a bad length, a
+ * node outside its tree or a bad page gets its status and out_len -1, and
+ * nothing of it is written. */
 typedef struct {
   int32_t B;
   int32_t total_nodes;

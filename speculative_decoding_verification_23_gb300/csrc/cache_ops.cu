@@ -128,10 +128,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   bad = __syncthreads_or(bad);
   int32_t* index = P.index + ((long long)b * P.heads + h) * P.keep;
   float* kept = P.kept ? P.kept + ((long long)b * P.heads + h) * P.keep : nullptr;
-  if (h == 0 && tid == 0) {
-    if (P.status) P.status[b] = !ok ? kStatusBadLen : (bad ? kStatusBadPage : 0);
-    P.new_len[b] = ok && !bad ? m : -1;
-  }
+  if (h == 0 && tid == 0 && P.status) P.status[b] = !ok ? kStatusBadLen : (bad ? kStatusBadPage : 0);
   ok = ok && !bad;
   for (int i = (ok ? m : 0) + tid; i < P.keep; i += kSelThreads) {
     index[i] = -1;
@@ -283,17 +280,24 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 // channels, 262 MB read and written, 41 us, 6.4 TB/s.  Threads per CTA, here
 // and for the path, 64 / 128 / 256 / 512: with the selection 82 / 59.0 / 59.9 /
 // 61.9 us, 64 requests' paths 19.4 / 17.3 / 16.9 / 20.5.
+//
+// The new lengths are written here, where every head's selection has ended, as
+// they may take the place of the lengths that it read.
 constexpr int kMoveThreads = 256;
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams P, int blocks) {
   const int part = blockIdx.x % blocks, bh = blockIdx.x / blocks;
   const int h = bh % P.heads, b = bh / P.heads;
   after_previous();
-  const int m = P.new_len[b];
   const int pieces = P.dim / 8, per = kMoveThreads / pieces;
   const int i = part * per + (int)threadIdx.x / pieces, ch = threadIdx.x % pieces;
-  if (i >= m || (int)threadIdx.x >= per * pieces) return;
+  if (i >= P.keep || (int)threadIdx.x >= per * pieces) return;
   const int j = P.index[((long long)b * P.heads + h) * P.keep + i];
+  const bool first = i == 0 && ch == 0 && h == 0;
+  if (j < 0) {  // past the kept tokens, or of an empty or bad request
+    if (first) P.new_len[b] = P.len[b] == 0 ? 0 : -1;
+    return;
+  }
   const PageDiv pd(P.page_size);
   int ps, ss, pt, st;
   pd.split(j, ps, ss);
@@ -306,12 +310,17 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
   const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.v) + from);
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.k) + to) = k;
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.v) + to) = v;
+  if (first) P.new_len[b] = min(P.len[b], P.keep);
 }
 
 // One CTA per (request, layer): checks the request, then copies its path.
 // Latency bounds it, lengths to table to rows: 64 requests' paths of up to 33
 // nodes in 28 layers of 4 heads of 128 channels, 89 MB read and written, 16.9
 // us, 5.3 TB/s; one request's path 5.4 us.
+//
+// New lengths that take the place of the old ones, which every layer reads, are
+// written by a launch of their own: P.new_len is null here, and there P.layers
+// is 0.
 __global__ void __launch_bounds__(kMoveThreads) commit_kernel(const CommitParams P) {
   after_previous();
   const int b = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x;
@@ -337,9 +346,9 @@ __global__ void __launch_bounds__(kMoveThreads) commit_kernel(const CommitParams
   if (layer == 0 && tid == 0) {
     const int st = (!ok || bad_node ? kStatusBadLen : 0) | (bad_page ? kStatusBadPage : 0);
     if (P.status) P.status[b] = st;
-    P.new_len[b] = st ? -1 : ctx + m;
+    if (P.new_len) P.new_len[b] = st ? -1 : ctx + m;
   }
-  if (!ok || bad_node || bad_page) return;
+  if (!ok || bad_node || bad_page || layer >= P.layers) return;
   // four pieces of keys and of values a thread in flight
   const int pieces = P.dim / 8, per_tok = P.heads * pieces, all = m * per_tok;
   constexpr int U = 4;
@@ -378,7 +387,14 @@ int launch_evict(const EvictParams& P, cudaStream_t s) {
 }
 
 int launch_commit(const CommitParams& P, cudaStream_t s) {
-  return launch_kernel(commit_kernel, dim3(P.B, P.layers), kMoveThreads, 0, s, P);
+  CommitParams Q = P;
+  const bool in_place = P.new_len == P.ctx && P.layers > 1;
+  if (in_place) Q.new_len = nullptr;
+  if (launch_kernel(commit_kernel, dim3(P.B, P.layers), kMoveThreads, 0, s, Q)) return -1;
+  if (!in_place) return 0;
+  Q.new_len = P.new_len;
+  Q.layers = 0;
+  return launch_kernel(commit_kernel, dim3(P.B), kMoveThreads, 0, s, Q);
 }
 
 }  // namespace sv

@@ -96,7 +96,7 @@ struct EvictParams {
   long long s_page, s_slot, s_head;
   int32_t* index;
   float* kept;      // or null
-  int32_t* new_len;
+  int32_t* new_len; // may be len
   int32_t* status;  // or null
   int B, keep, sink, recent, ld, ld_table, ld_to;
   int num_pages, page_size, heads, dim;
@@ -113,7 +113,7 @@ struct CommitParams {
   void* k;
   void* v;
   long long sn_layer, sn_node, sn_head, s_layer, s_page, s_slot, s_head;
-  int32_t* new_len;
+  int32_t* new_len;  // may be ctx
   int32_t* status;
   int B, total, layers, ld_path, ld_table;
   int num_pages, page_size, heads, dim;

@@ -372,7 +372,8 @@ def spec_cache_evict(args: SpecEvictArgs, *, out_index=None, out_kept=None, out_
                      stream=None):
     """Keeps the tokens of largest weight through ``spec_cache_evict`` and
     moves them to the new pages.  Returns (index [B, heads, keep] int32, kept
-    weights [B, heads, keep] float32, new lengths [B] int32, status [B])."""
+    weights [B, heads, keep] float32, new lengths [B] int32, status [B]).
+    `out_len` may be the block's kv_len."""
     import torch
 
     lib = _lib()
@@ -421,7 +422,8 @@ def make_commit_args(*, k_new, v_new, cu_nodes, path, path_len, cache: SpecCache
 
 def spec_cache_commit(args: SpecCommitArgs, *, out_len=None, out_status=None, stream=None):
     """Writes the accepted paths' keys and values to the cache through
-    ``spec_cache_commit``.  Returns (new lengths [B] int32, status [B])."""
+    ``spec_cache_commit``.  Returns (new lengths [B] int32, status [B]).
+    `out_len` may be the block's ctx_len."""
     import torch
 
     lib = _lib()
