@@ -339,8 +339,10 @@ def spec_attention_weights(args: SpecWeighArgs, before=None, *, ld=None, out=Non
         out = _empty(stream, *shape, dtype=torch.float32, like=_device())
     if out_status is None:
         out_status = _empty(stream, args.B, dtype=torch.int32, like=_device())
-    args.ld = int(ld)
-    rc = lib.spec_attention_weights(ctypes.byref(args), _ptr(before), _ptr(out), _ptr(out_status),
+    # the block stays as it is: another thread may call with it and another ld
+    call = SpecWeighArgs.from_buffer_copy(args)
+    call.ld = int(ld)
+    rc = lib.spec_attention_weights(ctypes.byref(call), _ptr(before), _ptr(out), _ptr(out_status),
                                     _stream_handle(stream))
     _raise(rc, "spec_attention_weights")
     return out, out_status
