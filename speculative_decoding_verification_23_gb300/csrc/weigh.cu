@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kWgWarps * 32) weigh_kernel(const WeighParams 
   const PageDiv pd(P.page_size);
   // key rows r0 and r0 + 8 of the fragments
   uint32_t kf[D / 16][4];
-  bool bad = false;
+  bool bad[2] = {false, false};  // a page of their own each
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int j = lo + (lane >> 2) + 8 * e;
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kWgWarps * 32) weigh_kernel(const WeighParams 
       pd.split(j, page, slot);
       const int id = P.table[(long long)b * P.ld_table + page];
       if (id < 0 || id >= P.num_pages)
-        bad = true;
+        bad[e] = true;
       else
         src = static_cast<const T*>(P.k) + (long long)id * P.s_page + (long long)slot * P.s_slot + (long long)h * P.s_head;
     }
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kWgWarps * 32) weigh_kernel(const WeighParams 
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int j = lo + (lane >> 2) + 8 * e;
-      if (j < P.ld) out[j] = !ok ? NAN : (j < len ? (bad ? NAN : (before ? before[j] : 0.f) + w[e]) : 0.f);
+      if (j < P.ld) out[j] = !ok ? NAN : (j < len ? (bad[e] ? NAN : (before ? before[j] : 0.f) + w[e]) : 0.f);
     }
   }
 }
