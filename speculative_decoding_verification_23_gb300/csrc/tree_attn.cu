@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kJoinOf<D> * 32) tree_join_kernel(const TreePa
   const int heads_q = P.heads * P.group;
   if (blockIdx.y == 0 && P.status) {
     int bad = 0;
-    if (r.ok && r.n > 0) {
+    if (r.ok) {
       const long long pages = ((long long)r.ctx + P.page_size - 1) / P.page_size;
       for (long long p = threadIdx.x; p < pages; p += kJoinWarps * 32) {
         const int id = P.table[(long long)b * P.ld_table + p];
