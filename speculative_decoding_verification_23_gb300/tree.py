@@ -496,21 +496,25 @@ def spec_beam_select(args: SpecBeamArgs, *, workspace=None, out_scores=None, out
     return tuple(got)
 
 
-def _state(src, dst, B, W, keep):
+def _state(src, dst, B, W, keep, layered):
     """``spec_beam_state`` of src [B, W, ...] or [outer, B, W, ...]."""
     for name, t in (("a state's source", src), ("a state's destination", dst)):
         if not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
     if src.dtype != dst.dtype or src.dim() != dst.dim():
         raise TypeError("a state's source and destination must have the same type and number of axes")
-    if tuple(src.shape[:2]) == (B, W) and tuple(dst.shape[:2]) == (B, keep) and src.shape[2:] == dst.shape[2:]:
-        lead = 0
-    elif (src.dim() >= 3 and tuple(src.shape[1:3]) == (B, W) and tuple(dst.shape[1:3]) == (B, keep)
-          and src.shape[0] == dst.shape[0] and src.shape[3:] == dst.shape[3:]):
-        lead = 1
-    else:
-        raise ValueError(f"a state must have shapes (..., {B}, {W}, ...) and (..., {B}, {keep}, ...) with at most one "
-                         f"axis before the request's, got {tuple(src.shape)} and {tuple(dst.shape)}")
+    fits = [tuple(src.shape[i:i + 2]) == (B, W) and tuple(dst.shape[i:i + 2]) == (B, keep)
+            and src.shape[:i] == dst.shape[:i] and src.shape[i + 2:] == dst.shape[i + 2:] for i in (0, 1)]
+    if layered is not None:
+        fits[not layered] = False
+    if all(fits):
+        raise ValueError(f"a state of shape {tuple(src.shape)} may or may not have an axis before the request's: "
+                         f"say which by `layered`")
+    if not any(fits):
+        raise ValueError(f"a state must have shapes (..., {B}, {W}, ...) and (..., {B}, {keep}, ...) with "
+                         f"{'at most one' if layered is None else 'one' if layered else 'no'} axis before the "
+                         f"request's, got {tuple(src.shape)} and {tuple(dst.shape)}")
+    lead = int(fits[1])
     rest = 1
     for n, s, d in zip(reversed(src.shape[lead + 2:]), reversed(src.stride()[lead + 2:]),
                        reversed(dst.stride()[lead + 2:])):
@@ -526,16 +530,22 @@ def _state(src, dst, B, W, keep):
     return a
 
 
-def make_reorder_args(*, parents, beams: int, states) -> ReorderArgs:
+def make_reorder_args(*, parents, beams: int, states, layered=None) -> ReorderArgs:
     """The arguments of ``spec_beam_reorder``: parents [B, keep] int32 and
     pairs (source [B, beams, ...], destination [B, keep, ...]), or both with
-    one axis (layers) before the request's."""
+    one axis (layers) before the request's.  `layered` says whether states
+    have that axis: True, False, a sequence of these for each state, or None,
+    where shapes tell; a shape that fits both forms is refused then."""
     _check_i32("parents", parents)
     if parents.dim() != 2:
         raise ValueError(f"parents must have shape (B, keep), got {tuple(parents.shape)}")
     B, keep = parents.shape
     states = list(states)
-    block = (SpecBeamState * max(1, len(states)))(*(_state(s, d, B, int(beams), keep) for s, d in states))
+    forms = [layered] * len(states) if layered is None or isinstance(layered, bool) else list(layered)
+    if len(forms) != len(states):
+        raise ValueError(f"layered must have one value for each of {len(states)} states, got {len(forms)}")
+    block = (SpecBeamState * max(1, len(states)))(*(_state(s, d, B, int(beams), keep, f)
+                                                    for (s, d), f in zip(states, forms)))
     return ReorderArgs(B, int(beams), keep, parents, (block, len(states)), (parents, states))
 
 
