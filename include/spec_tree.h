@@ -21,6 +21,11 @@
  * enqueues nothing; data errors found on the device go to out_status [B]
  * (may be NULL) as an OR of SPEC_STATUS_* and never trap.  A captured call
  * replays with the contents that its buffers then have.
+ *
+ * A call's results overlap nothing that it reads, and one another neither,
+ * except where an entry point says so: its CTAs do not begin together, and one
+ * could find another's results for its arguments.  Scores, lengths, tables and
+ * weights that results overlap are refused with SPEC_ERR_SHAPE.
  */
 #ifndef SPEC_TREE_H
 #define SPEC_TREE_H

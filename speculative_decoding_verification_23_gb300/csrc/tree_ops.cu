@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
@@ -119,6 +120,23 @@ sv::TreePlan plan_tree(const spec_tree_args* a, int num_sms) {
   return fits && rows > kWarpRows ? sv::plan_tree_tc(rows, num_sms) : sv::plan_tree_warp(c.dim, num_sms);
 }
 
+// Memory that a call reads or writes: n elements of 4 bytes, or of `size`.
+struct Span {
+  uintptr_t at;
+  unsigned long long bytes;
+  Span(const void* p, long long n, int size = 4)
+      : at(reinterpret_cast<uintptr_t>(p)), bytes(p ? (unsigned long long)n * size : 0ull) {}
+};
+
+// Whether results overlap anything that a kernel reads: CTAs do not begin
+// together, so one could find results of another for arguments.
+bool overlap(std::initializer_list<Span> out, std::initializer_list<Span> in) {
+  for (const Span& o : out)
+    for (const Span& i : in)
+      if (o.bytes > 0 && i.bytes > 0 && o.at < i.at + i.bytes && i.at < o.at + o.bytes) return true;
+  return false;
+}
+
 uint16_t* layer_of(void* p, const spec_cache& c, int layer) {
   return static_cast<uint16_t*>(p) + (long long)layer * c.s_layer;
 }
@@ -151,6 +169,10 @@ int spec_tree_attention(const spec_tree_args* a, void* out, int64_t so_node, int
   const sv::TreeWorkspace W = sv::make_tree_workspace(a->B, plan.grid, plan.rows, a->cache.dim);
   if (ws_bytes < W.total) return SPEC_ERR_WORKSPACE;
   if (rc) return rc;
+  if (overlap({{out_lse, (long long)a->total_nodes * a->heads_q}, {out_status, a->B}},
+              {{a->cu_nodes, a->B + 1ll}, {a->ctx_len, a->B}, {a->block_table, (long long)a->B * a->ld_table},
+               {a->tree_mask, (long long)a->total_nodes * a->mask_words}}))
+    return SPEC_ERR_SHAPE;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   unsigned char* w = static_cast<unsigned char*>(workspace);
   sv::TreeParams P;
@@ -221,9 +243,13 @@ int spec_attention_weights(const spec_weigh_args* a, const float* before, float*
   int sms = 0;
   rc = sm_count(&sms);
   if (rc) return rc;
+  const spec_cache& c = a->cache;
+  const long long keys = (long long)a->B * c.heads * a->ld, lens = a->B;
+  const Span before_at(before == out ? nullptr : before, keys), lse_at(a->lse, (long long)a->total_rows * a->heads_q),
+      cu_at(a->cu_rows, lens + 1), len_at(a->kv_len, lens), table_at(a->block_table, lens * a->ld_table);
+  if (overlap({{out, keys}, {out_status, lens}}, {before_at, lse_at, cu_at, len_at, table_at})) return SPEC_ERR_SHAPE;
   const bool bf16 = a->cache.dtype == SPEC_BF16;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const spec_cache& c = a->cache;
   const long long rows = (long long)a->max_rows * (a->heads_q / c.heads);
   // Tensor memory where its rows and tiles fit: on 16 requests of up to 16384
   // tokens, 8 key heads of 128 channels, 4 / 36 / 128 rows per key head, 60.8 /
@@ -308,6 +334,12 @@ int spec_cache_evict(const spec_evict_args* a, int32_t* out_index, float* out_ke
   int sms = 0;
   rc = sm_count(&sms);
   if (rc) return rc;
+  const long long rows = (long long)a->B * a->cache.heads, kept = rows * a->keep;
+  if (overlap({{out_index, kept}, {out_kept, kept}, {out_len, a->B}, {out_status, a->B}},
+              {{a->weights, rows * a->ld}, {out_len == a->kv_len ? nullptr : a->kv_len, a->B},
+               {a->block_table, (long long)a->B * a->ld_table}, {a->to_table, (long long)a->B * a->ld_to}}) ||
+      overlap({{out_index, kept}, {out_kept, kept}, {out_status, a->B}}, {{a->kv_len, a->B}}))
+    return SPEC_ERR_SHAPE;
   sv::EvictParams P;
   std::memset(&P, 0, sizeof(P));
   P.weights = a->weights;
@@ -355,6 +387,12 @@ int spec_cache_commit(const spec_commit_args* a, int32_t* out_len, int32_t* out_
   int sms = 0;
   rc = sm_count(&sms);
   if (rc) return rc;
+  const long long lens = a->B;
+  if (overlap({{out_len, lens}, {out_status, lens}},
+              {{a->cu_nodes, lens + 1}, {a->path, lens * a->ld_path}, {a->path_len, lens},
+               {a->block_table, lens * a->ld_table}, {out_len == a->ctx_len ? nullptr : a->ctx_len, lens}}) ||
+      overlap({{out_status, lens}}, {{a->ctx_len, lens}}))
+    return SPEC_ERR_SHAPE;
   sv::CommitParams P;
   std::memset(&P, 0, sizeof(P));
   P.cu = a->cu_nodes;
@@ -444,6 +482,11 @@ int spec_beam_select(const spec_beam_args* a, float* out_scores, int32_t* out_pa
   const sv::BeamWorkspace W = sv::make_beam_workspace(a->B, a->W, P.grid, P.spans, P.chunks);
   if (ws_bytes < W.total) return SPEC_ERR_WORKSPACE;
   if (rc) return rc;
+  const long long rows = (long long)a->B * a->W, kept = (long long)a->B * a->keep;
+  if (overlap({{out_scores, kept}, {out_parents, kept}, {out_tokens, kept}, {out_status, a->B}},
+              {{a->scores, rows}, {a->finished, rows},
+               {a->logits, (rows - 1) * a->ld + a->V, a->dtype == SPEC_BF16 ? 2 : 4}}))
+    return SPEC_ERR_SHAPE;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   unsigned char* w = static_cast<unsigned char*>(workspace);
   P.logits = a->logits;
