@@ -888,7 +888,9 @@ int launch_beam_select(const BeamParams& P, bool bf16, cudaStream_t s) {
               : launch_kernel(beam_select_kernel<float>, dim3(P.grid), kBmThreads, bytes, s, P);
 }
 
-// Fills the work split of P's states and returns the number of blocks.
+// Fills the work split of P's states and returns the number of blocks, or one
+// past 32 bits (a state has at most 2^31 rows of 2^30 blocks, so that the sum
+// is not taken further).
 long long plan_reorder(ReorderParams& P) {
   long long at = 0;
   for (int k = 0; k < P.num; ++k) {
@@ -897,6 +899,7 @@ long long plan_reorder(ReorderParams& P) {
     s.blocks = (int)((n + per - 1) / per);
     s.first = at;
     at += (long long)s.blocks * s.outer * P.B * P.keep;
+    if (at > INT32_MAX) break;
   }
   return at;
 }

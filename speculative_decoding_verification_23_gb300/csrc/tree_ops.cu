@@ -73,6 +73,9 @@ constexpr int kMaxTokens = INT32_MAX - 65535;
 bool table_ok(int ld, int page_size) { return ld >= 1 && (long long)ld * page_size <= kMaxTokens; }
 bool row_ok(int ld) { return ld >= 1 && ld <= kMaxTokens; }
 
+// a b c <= most, of positive factors whose product may pass 64 bits.
+bool fits32(long long a, long long b, long long c, long long most = INT32_MAX) { return a <= most / b && a * b <= most / c; }
+
 int check_tree(const spec_tree_args* a) {
   if (!a) return SPEC_ERR_NULL;
   int rc = check_cache(a->cache, true);
@@ -329,7 +332,7 @@ int spec_cache_evict(const spec_evict_args* a, int32_t* out_index, float* out_ke
   if (!table_ok(a->ld_table, a->cache.page_size) || !table_ok(a->ld_to, a->cache.page_size)) return SPEC_ERR_SHAPE;
   if ((long long)a->ld_to * a->cache.page_size < a->keep) return SPEC_ERR_SHAPE;
   // CTAs of the move: at least 8 kept tokens each
-  if ((long long)a->B * a->cache.heads * ((a->keep + 7) / 8) > INT32_MAX) return SPEC_ERR_SHAPE;
+  if (!fits32(a->B, a->cache.heads, (a->keep + 7) / 8)) return SPEC_ERR_SHAPE;
   if (!a->weights || !a->kv_len || !a->block_table || !a->to_table || !out_index || !out_len) return SPEC_ERR_NULL;
   int sms = 0;
   rc = sm_count(&sms);
@@ -375,7 +378,7 @@ int spec_cache_commit(const spec_commit_args* a, int32_t* out_len, int32_t* out_
   int rc = check_cache(a->cache, true);
   if (rc) return rc;
   if (a->B < 1 || a->total_nodes < 0 || a->ld_path < 1 || a->cache.layers > 65535) return SPEC_ERR_SHAPE;
-  if ((long long)a->ld_path * a->cache.heads * (a->cache.dim / 8) > kMaxTokens) return SPEC_ERR_SHAPE;
+  if (!fits32(a->ld_path, a->cache.heads, a->cache.dim / 8, kMaxTokens)) return SPEC_ERR_SHAPE;
   if (!table_ok(a->ld_table, a->cache.page_size)) return SPEC_ERR_SHAPE;
   if (!a->cu_nodes || !a->path || !a->path_len || !a->block_table || !a->ctx_len || !out_len) return SPEC_ERR_NULL;
   if (a->total_nodes > 0) {
@@ -521,6 +524,8 @@ int spec_beam_reorder(int32_t B, int32_t W, int32_t keep, const int32_t* parents
     const spec_beam_state& a = states[i];
     if (a.row_bytes < 0 || a.outer < 0 || a.row_bytes > (1ll << 40)) return SPEC_ERR_SHAPE;
     if (a.row_bytes > 0 && a.outer > 0 && (!a.src || !a.dst)) return SPEC_ERR_NULL;
+    // a block at least for every row
+    if (a.row_bytes > 0 && a.outer > 0 && !fits32(B, keep, a.outer)) return SPEC_ERR_SHAPE;
     sv::BeamState& s = P.s[i];
     s.src = static_cast<const unsigned char*>(a.src);
     s.dst = static_cast<unsigned char*>(a.dst);
