@@ -163,6 +163,13 @@ def _check_out(name, t, shape, dtype):
         raise TypeError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
 
 
+def _workspace_bytes(t):
+    """The size of a caller's workspace, of any type."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise TypeError("a workspace must be a contiguous CUDA tensor")
+    return t.numel() * t.element_size()
+
+
 def _kv_dtype(t):
     import torch
 
@@ -275,6 +282,7 @@ def spec_tree_attention(args: SpecTreeArgs, *, workspace=None, out=None, out_lse
     shape = (args.total_nodes, args.heads_q, args.cache.dim)
     if workspace is None:
         workspace = make_tree_workspace(args, stream)
+    ws_bytes = _workspace_bytes(workspace)
     if out is None:
         out = _empty(stream, *shape, dtype=args.torch_dtype, like=workspace.device)
     else:
@@ -289,7 +297,7 @@ def spec_tree_attention(args: SpecTreeArgs, *, workspace=None, out=None, out_lse
     else:
         _check_out("out_status", out_status, (args.B,), torch.int32)
     rc = lib.spec_tree_attention(ctypes.byref(args), _ptr(out), out.stride(0), out.stride(1), _ptr(out_lse),
-                                 _ptr(out_status), _ptr(workspace), workspace.numel(), _stream_handle(stream))
+                                 _ptr(out_status), _ptr(workspace), ws_bytes, _stream_handle(stream))
     _raise(rc, "spec_tree_attention")
     return out, out_lse, out_status
 
@@ -482,6 +490,7 @@ def spec_beam_select(args: SpecBeamArgs, *, workspace=None, out_scores=None, out
     lib = _lib()
     if workspace is None:
         workspace = make_beam_workspace(args, stream)
+    ws_bytes = _workspace_bytes(workspace)
     shape = (args.B, args.keep)
     got = []
     for name, t, sh, dt in (("out_scores", out_scores, shape, torch.float32),
@@ -490,7 +499,7 @@ def spec_beam_select(args: SpecBeamArgs, *, workspace=None, out_scores=None, out
                             ("out_status", out_status, shape[:1], torch.int32)):
         _check_out(name, t, sh, dt)
         got.append(_empty(stream, *sh, dtype=dt, like=workspace.device) if t is None else t)
-    rc = lib.spec_beam_select(ctypes.byref(args), *(_ptr(t) for t in got), _ptr(workspace), workspace.numel(),
+    rc = lib.spec_beam_select(ctypes.byref(args), *(_ptr(t) for t in got), _ptr(workspace), ws_bytes,
                               _stream_handle(stream))
     _raise(rc, "spec_beam_select")
     return tuple(got)
