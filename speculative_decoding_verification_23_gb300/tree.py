@@ -126,6 +126,15 @@ def _raise(rc, where):
         raise SpecError(rc, where)
 
 
+def _int32(name, x) -> int:
+    """A whole number that its field holds: ctypes keeps the low 32 bits of
+    any."""
+    x = int(x)
+    if not -1 << 31 <= x < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 def _stream_handle(stream) -> int:
     """The stream's handle; the current one is asked for without building the
     Python object around it, which costs more than a launch."""
@@ -249,7 +258,8 @@ def make_tree_args(*, q, k_new, v_new, cu_nodes, max_nodes: int, cache: SpecCach
         if tree_mask.dim() != 2 or tree_mask.shape[0] != total:
             raise ValueError(f"tree_mask must have shape ({total}, words), got {tuple(tree_mask.shape)}")
         a.tree_mask, a.mask_words = _ptr(tree_mask), tree_mask.shape[1]
-    a.B, a.total_nodes, a.max_nodes, a.heads_q, a.layer = B, total, int(max_nodes), q.shape[1], int(layer)
+    a.B, a.total_nodes, a.max_nodes, a.heads_q = B, total, _int32("max_nodes", max_nodes), q.shape[1]
+    a.layer = _int32("layer", layer)
     a.scale = cache.dim ** -0.5 if scale is None else float(scale)
     a.cu_nodes, a.q, a.k_new, a.v_new = _ptr(cu_nodes), _ptr(q), _ptr(k_new), _ptr(v_new)
     a.sq_node, a.sq_head = q.stride()[:2]
@@ -317,7 +327,8 @@ def make_weigh_args(*, q, lse, cu_rows, max_rows: int, cache: SpecCache, block_t
     _check_table("block_table", block_table, B)
     _check_lengths("kv_len", kv_len, B)
     a = SpecWeighArgs()
-    a.B, a.total_rows, a.max_rows, a.heads_q, a.layer = B, q.shape[0], int(max_rows), q.shape[1], int(layer)
+    a.B, a.total_rows, a.max_rows, a.heads_q = B, q.shape[0], _int32("max_rows", max_rows), q.shape[1]
+    a.layer = _int32("layer", layer)
     a.scale = cache.dim ** -0.5 if scale is None else float(scale)
     a.cu_rows, a.q, a.lse = _ptr(cu_rows), _ptr(q), _ptr(lse)
     a.sq_row, a.sq_head = q.stride()[:2]
@@ -339,7 +350,7 @@ def spec_attention_weights(args: SpecWeighArgs, before=None, *, ld=None, out=Non
     ld = given.shape[-1] if given is not None else ld
     if ld is None:
         raise ValueError("the row length ld is needed where neither before nor out is given")
-    shape = (args.B, args.cache.heads, int(ld))
+    shape = (args.B, args.cache.heads, _int32("ld", ld))
     _check_out("before", before, shape, torch.float32)
     _check_out("out", out, shape, torch.float32)
     _check_out("out_status", out_status, (args.B,), torch.int32)
@@ -349,7 +360,7 @@ def spec_attention_weights(args: SpecWeighArgs, before=None, *, ld=None, out=Non
         out_status = _empty(stream, args.B, dtype=torch.int32, like=_device())
     # the block stays as it is: another thread may call with it and another ld
     call = SpecWeighArgs.from_buffer_copy(args)
-    call.ld = int(ld)
+    call.ld = shape[2]
     rc = lib.spec_attention_weights(ctypes.byref(call), _ptr(before), _ptr(out), _ptr(out_status),
                                     _stream_handle(stream))
     _raise(rc, "spec_attention_weights")
@@ -370,7 +381,8 @@ def make_evict_args(*, weights, kv_len, keep: int, cache: SpecCache, block_table
     _check_table("block_table", block_table, B)
     _check_table("to_table", to_table, B)
     a = SpecEvictArgs()
-    a.B, a.keep, a.sink, a.recent, a.layer, a.ld = B, int(keep), int(sink), int(recent), int(layer), weights.shape[2]
+    a.B, a.keep, a.ld = B, _int32("keep", keep), weights.shape[2]
+    a.sink, a.recent, a.layer = _int32("sink", sink), _int32("recent", recent), _int32("layer", layer)
     a.weights, a.kv_len, a.cache = _ptr(weights), _ptr(kv_len), cache
     a.block_table, a.ld_table = _ptr(block_table), block_table.shape[1]
     a.to_table, a.ld_to = _ptr(to_table), to_table.shape[1]
@@ -463,7 +475,8 @@ def make_beam_args(*, logits, V: int, scores, keep: int, finished=None, end_toke
         _check_i32("finished", finished)
         _check_shape("finished", finished, (B, W))
     a = SpecBeamArgs()
-    a.B, a.W, a.keep, a.V, a.dtype, a.end_token = B, W, int(keep), int(V), _dtype_code(logits), int(end_token)
+    a.B, a.W, a.keep, a.V, a.dtype = B, W, _int32("keep", keep), _int32("V", V), _dtype_code(logits)
+    a.end_token = _int32("end_token", end_token)
     a.logits, a.ld = _ptr(logits), logits.stride(0)
     a.scores, a.finished = _ptr(scores), _ptr(finished)
     a._keep = (logits, scores, finished)
@@ -549,13 +562,14 @@ def make_reorder_args(*, parents, beams: int, states, layered=None) -> ReorderAr
     if parents.dim() != 2:
         raise ValueError(f"parents must have shape (B, keep), got {tuple(parents.shape)}")
     B, keep = parents.shape
+    W = _int32("beams", beams)
     states = list(states)
     forms = [layered] * len(states) if layered is None or isinstance(layered, bool) else list(layered)
     if len(forms) != len(states):
         raise ValueError(f"layered must have one value for each of {len(states)} states, got {len(forms)}")
-    block = (SpecBeamState * max(1, len(states)))(*(_state(s, d, B, int(beams), keep, f)
+    block = (SpecBeamState * max(1, len(states)))(*(_state(s, d, B, W, keep, f)
                                                     for (s, d), f in zip(states, forms)))
-    return ReorderArgs(B, int(beams), keep, parents, (block, len(states)), (parents, states))
+    return ReorderArgs(B, W, keep, parents, (block, len(states)), (parents, states))
 
 
 def spec_beam_reorder(args: ReorderArgs, *, stream=None):
