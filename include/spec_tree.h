@@ -84,7 +84,10 @@ typedef struct {
  * infinities included.  Statistics and sums are fp32; the weights are rounded
  * to the cache's type for their product with the values (unnormalised, the
  * row's running maximum between 1 and 2^8; with SPEC_F16 weights below 2^-14
- * round to multiples of 2^-24), the result once more.
+ * round to multiples of 2^-24), the result once more.  The divisor may hold the
+ * largest weight of every 64 keys as rounded.  So with p_j = exp(s_j - lse) an
+ * output is off by at most half a step of sum_j p_j |v_j| + 2 |out|, beside what
+ * fp32 sums and exponentials add.
  *
  * A request with a bad length or page gets its status, and NaN in its rows
  * of out and lse. */
@@ -213,15 +216,16 @@ int spec_cache_commit(const spec_commit_args *args, int32_t *out_len, int32_t *o
  *   scores[b, w] + z_v - log sum_u exp(z_u);
  *
  * an ended beam (finished[b, w] != 0) has one continuation, end_token, with
- * its own score, and its logits are not read.  Kept are the `keep` best
- * continuations of a request, best first, ties to the lowest w*V + v.  Where
- * there are fewer (a score of -inf, logits of -inf), the rest has score
- * -inf, parent -1 and token -1.  Scores are compared in 64 bits (row sums of
- * fp32 exponentials, within 2^-21 of the score), so beams whose scores are
- * nearer than that may take either order, and rounded once.  A NaN or +inf logit or score gives
- * the request SPEC_STATUS_BAD_LOGITS, scores -inf, parents and tokens -1; a
- * logit from 2.3e38 on, which leaves fp32 once scaled by log2(e), counts as
- * +inf. */
+ * its own score.  The logits of an ended beam, and of one of score -inf, are
+ * not read.  Kept are the `keep` best continuations of a request, best first,
+ * ties to the lowest w*V + v.  Where there are fewer (a score of -inf, logits of
+ * -inf), the rest has score -inf, parent -1 and token -1.  Scores are compared
+ * in 64 bits (row sums of fp32 exponentials, within 2^-21 of the score), so
+ * continuations of different beams whose scores are nearer than that, or equal,
+ * may take either order, and rounded once.  A NaN or +inf logit that is read, or
+ * such a score, gives the request SPEC_STATUS_BAD_LOGITS, scores -inf, parents
+ * and tokens -1; a logit from 2.3e38 on, which leaves fp32 once scaled by
+ * log2(e), counts as +inf. */
 typedef struct {
   int32_t B;
   int32_t W;           /* beams, 1 .. SPEC_MAX_BEAMS                         */

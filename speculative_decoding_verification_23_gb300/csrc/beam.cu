@@ -707,10 +707,12 @@ __device__ __forceinline__ void beam_finish(const BeamParams& P, BeamShared& sh,
 // One wave of CTAs, each with an even share of all logits that are read; the
 // last CTA of a request to arrive picks its continuations.
 //
-// 64 x 8 beams over 152064 bf16 logits, 158 MB: the logits are read in about 30
-// us (loads, exponentials and their issue), the last requests' continuations
-// take 12 us after that, dependent trips to L2 by one CTA a request, and the
-// beams' states 5 us; 48 us in all.  4 beams of one request: 15 us, latency.
+// 64 x 8 beams over 152064 bf16 logits, 156 MB: 46 us, and 49 with the beams'
+// states.  Without the continuations, dependent trips to L2 by one CTA a
+// request, 37; of these without exponentials 36.4, without any sums 35.8, and
+// then with twice as many loads in flight 34.2: the stream is bound by its loads
+// in flight, its start and its end, not by what it computes.  4 beams of one
+// request: 15 us, latency.
 template <typename T>
 __global__ void __launch_bounds__(kBmThreads, kBmCtas) beam_select_kernel(const BeamParams P) {
   using S = BmShape<T>;

@@ -76,8 +76,9 @@ __device__ __noinline__ uint32_t select_long(const float* w, int lo, int hi, int
 // keys are left between the bounds; these go to a list, where ranks decide.
 // Barriers and comparisons bound it, not bytes: 16 requests of 8 heads and up to
 // 16384 tokens, 128 CTAs, take 15 us for 5 MB.  Bit by bit, one request cut from
-// 4000 tokens takes 14.4 us with its move, two by two 13.4; of 16384 tokens both
-// take as long.
+// 4000 tokens takes 14.4 us with its move, two by two 13.4 (on the device alone;
+// 15 to 17 with what launches from the host add); of 16384 tokens both take as
+// long.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams P) {
   __shared__ int counts[2][kSelThreads / 32];
   __shared__ uint32_t list[kSelList];

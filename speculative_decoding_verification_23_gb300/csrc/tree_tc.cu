@@ -96,12 +96,16 @@ __device__ __noinline__ void add_odd(const TreeParams& P, int cu, int n, int nod
 // tile, and each has one buffer: the next tile's scores take its halves one
 // by one.
 //
-// What bounds it: with NT = 1 the copies (two contexts of 128 K tokens: 157 us
-// in all, 92 % of the copy rate; 64 requests' chains of up to 9 tokens, 63 rows
-// per key head: 72 us, 62 %, the rest being the ends of items, their drafted
-// tiles, the launch and the joining kernel); with NT = 2 the softmax, about
-// 1.5 us per tile of 256 rows and 128 keys, where the copies would take as
-// long (16 requests' trees of up to 64 nodes: 89 us, 760 TFLOP/s).
+// What bounds it.  With NT = 1 the copies: two contexts of 128 K tokens take
+// 157 us in all, 92 % of the copy rate.  64 requests' chains of up to 9 tokens,
+// 63 rows per key head, take 72 us, 62 %; of a CTA's 123 thousand cycles (the
+// slowest one's 136) 99 go to its 31.5 tiles, near the copy rate, 9 to loading
+// the queries of its 2.9 segments, 6 to their ends and 5 to the start, and the
+// joining kernel comes after.  With NT = 2, 16 requests' trees of up to 64
+// nodes, 89 us, 760 TFLOP/s: of 143 thousand cycles (the slowest 158) 113 go to
+// 33 tiles of 256 rows and 128 keys, 1.7 us each, of which 15 wait for scores
+// (the copies alone would take 1.5 us a tile), 13 to queries, 8 to segments'
+// ends and 4 to the start; the launch and the joining kernel take the rest.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     tree_tc_kernel(const TreeParams P, const __grid_constant__ TcMaps maps, int box) {
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
       ok = warp_wait(&o_last[w], seg & 1);
       if (!ok) break;
       tc_fence_after();
-      if (NT > 1) {  // odd_seg is written by the first row tile's threads
+      if (NT > 1) {  // odd_seg may be written by either row tile's threads
         mbar_arrive(&seg_end);
         ok = warp_wait(&seg_end, seg & 1);
         if (!ok) break;
