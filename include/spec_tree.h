@@ -222,7 +222,8 @@ int spec_cache_commit(const spec_commit_args *args, int32_t *out_len, int32_t *o
  * -inf), the rest has score -inf, parent -1 and token -1.  Scores are compared
  * in 64 bits (row sums of fp32 exponentials, within 2^-21 of the score), so
  * continuations of different beams whose scores are nearer than that, or equal,
- * may take either order, and rounded once.  A NaN or +inf logit that is read, or
+ * may take either order, and rounded once.  The only finite logit of a row, or
+ * one that all others leave no bit of, leaves the beam's score as it is.  A NaN or +inf logit that is read, or
  * such a score, gives the request SPEC_STATUS_BAD_LOGITS, scores -inf, parents
  * and tokens -1; a logit from 2.3e38 on, which leaves fp32 once scaled by
  * log2(e), counts as +inf. */

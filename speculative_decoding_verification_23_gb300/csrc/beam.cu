@@ -17,6 +17,7 @@ constexpr int kBmUnroll = 4;
 constexpr int kBmCtas = 2;
 constexpr int kBmCap = 2048;      // candidates of a request in shared memory
 constexpr int kBmHot = 1024;      // chunks that may hold candidates
+constexpr float kBmBad = 1.f, kBmLowest = 2.f;  // a piece's flags: no number, nothing but masks
 constexpr int kBeamRows = 2048;   // rows up to which those that are read are counted
 
 // A chunk is what a warp reads at once (1024 bf16 or 512 fp32 logits); a step
@@ -181,7 +182,7 @@ struct BeamShared {
   int place[kBeamMax];                       // of each row of the request in the split, -1: not read
   int pieces[kBeamMax];
   double lse[kBeamMax], row_sum[kBeamMax];
-  float row_ref[kBeamMax], s0[kBeamMax], add[kBeamMax], err[kBeamMax], z_min[kBeamMax];
+  float row_ref[kBeamMax], row_top[kBeamMax], s0[kBeamMax], add[kBeamMax], err[kBeamMax], z_min[kBeamMax];
   int row_low[kBeamMax];
   unsigned long long best_key[kBeamMax];     // the best K, in order
   int best_flat[kBeamMax];
@@ -290,7 +291,8 @@ __device__ __forceinline__ void beam_piece(const BeamParams& P, BeamShared& sh, 
     for (int w = 1; w < kBmWarps; ++w) M = fmaxf(M, sh.w_ref[w]);
     for (int w = 0; w < kBmWarps; ++w)
       sum_all += sh.w_ref[w] > -INFINITY ? sh.w_sum[w] * pow2_int(sh.w_ref[w] - M) : sh.w_sum[w];
-    __stcg(stat, make_float4(lowest ? best : M, sum_all, sum_all <= 3.4028235e38f ? 0.f : 1.f, lowest ? 1.f : 0.f));
+    const float flags = (sum_all <= 3.4028235e38f ? 0.f : kBmBad) + (lowest ? kBmLowest : 0.f);
+    __stcg(stat, make_float4(lowest ? best : M, sum_all, flags, best));
   }
 }
 
@@ -435,7 +437,7 @@ __device__ __forceinline__ void beam_finish(const BeamParams& P, BeamShared& sh,
     const float s0 = in ? P.scores[b * P.W + w] : 0.f;
     const int a = in ? sh.place[w] : -1, n = a >= 0 ? sh.pieces[w] : 0, cta = a >= 0 ? sp.first_cta(a) : 0;
     // sums of whole references, and of masks alone
-    float M = -INFINITY, M_low = -INFINITY;
+    float M = -INFINITY, M_low = -INFINITY, top = -INFINITY;
     double sum = 0.0, sum_low = 0.0;
     int off = !(s0 < INFINITY);
 #pragma unroll 1
@@ -446,9 +448,10 @@ __device__ __forceinline__ void beam_finish(const BeamParams& P, BeamShared& sh,
         v[j] = i + 8 * j < n ? __ldcg(P.stat + sp.record(cta + i + 8 * j, a, P.spans)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        off |= v[j].z != 0.f;
+        off |= v[j].z == kBmBad || v[j].z == kBmBad + kBmLowest;
         if (!(v[j].y > 0.f)) continue;
-        if (v[j].w == 0.f) {
+        top = fmaxf(top, v[j].w);
+        if (v[j].z < kBmLowest) {
           const float to = fmaxf(M, v[j].x);
           sum = sum * (double)pow2_int(M - to) + (double)(v[j].y * pow2_int(v[j].x - to));
           M = to;
@@ -464,6 +467,7 @@ __device__ __forceinline__ void beam_finish(const BeamParams& P, BeamShared& sh,
     for (int o = 4; o > 0; o >>= 1) {
       M_all = fmaxf(M_all, __shfl_xor_sync(0xffffffffu, M_all, o));
       low_all = fmaxf(low_all, __shfl_xor_sync(0xffffffffu, low_all, o));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     }
     const bool low_row = !(M_all > -INFINITY);  // nothing but the lowest logits
     if (low_row)
@@ -478,6 +482,7 @@ __device__ __forceinline__ void beam_finish(const BeamParams& P, BeamShared& sh,
       sh.row_sum[w] = sum;
       sh.row_ref[w] = low_row ? low_all : M_all;
       sh.row_low[w] = low_row;
+      sh.row_top[w] = top;
     }
   }
   __syncthreads();
@@ -495,7 +500,13 @@ __device__ __forceinline__ void beam_finish(const BeamParams& P, BeamShared& sh,
       l2 = (double)((int)(bits >> 52) - 1023) + (double)log2f(mf) + (double)((float)(m - (double)mf) / mf * L);
     }
     constexpr double inv = 1.0 / 1.4426950216293335;  // of that constant
-    const double lse = sh.row_low[w] ? (double)sh.row_ref[w] + l2 * inv : ((double)sh.row_ref[w] + l2) * inv;
+    // It is the largest logit at least, and is that logit where the sum is its
+    // term alone, computed as there (its lane's reference moved to it): one
+    // allowed token leaves a beam's score as it is.
+    const float top = sh.row_top[w];
+    double lse = sh.row_low[w] ? (double)sh.row_ref[w] + l2 * inv : ((double)sh.row_ref[w] + l2) * inv;
+    const bool alone = !sh.row_low[w] && sh.row_sum[w] == (double)ex2(fmaf(top, L, -sh.row_ref[w]));
+    if (alone || lse < (double)top) lse = (double)top;
     const float s0 = sh.s0[w];
     sh.lse[w] = lse;
     sh.add[w] = (float)((double)s0 - lse);

@@ -133,7 +133,7 @@ struct BeamParams {
   int32_t* status;
   unsigned long long* counters;  // [B] arrivals, call-tagged
   unsigned long long tag;
-  float4* stat;                  // [grid * spans] (reference, sum, bad, of masks alone)
+  float4* stat;                  // [grid * spans] (reference, sum, flags, largest logit)
   float* maxima;                 // [B * W][chunks]
   int B, W, keep, V, end_token;
   int grid, spans, chunks;       // CTAs, the most pieces of rows in one, chunks of a row
