@@ -20,37 +20,50 @@ struct WeighShape {
 };
 
 // The weights of requests without rows, by 128 threads: those of before, or 0.
-// All their keys, kIdle at a time, over the CTAs in turn.  16 requests of 8
-// heads and 16384 tokens, every second one without rows, kIdle 4096 / 1024 /
-// 512: 100 / 89 / 90 us, 104 with rows in all.  Not inlined, the call costs the
-// batch of the comment below 1.5 us, whether made or not.
+// Units of kIdle keys of a head, over the CTAs in turn; a warp looks at 32
+// requests at once.  16 requests of 8 heads and 16384 tokens, every second one
+// without rows, 87 us, 103 with rows in all (units of 4096 keys cost 11 us more,
+// of 512 one); 1024 of 500 tokens, one without rows, 331 us, 321 with rows in
+// all.  Not inlined, the call costs the batch of the comment below 1.5 us,
+// whether made or not.
 constexpr int kIdle = 1024;
 __device__ __forceinline__ void weigh_idle(const TreeParams& P, const float* before, float* out, int tid) {
   const PageDiv pd(P.page_size);
-  const int parts = (P.ld + kIdle - 1) / kIdle;
-  for (long long u = blockIdx.x; u < (long long)P.B * P.heads * parts; u += gridDim.x) {
-    const long long row = u / parts;
-    const int b = (int)(row / P.heads), lo = (int)(u - row * parts) * kIdle;
-    const TreeReq r = tree_request(P, b);
-    if (!r.ok || r.n > 0) continue;
-    const int hi = min(r.ctx, lo + kIdle);
-    const int32_t* table = P.table + (long long)b * P.ld_table;
-    for (int j0 = lo + tid; j0 < hi; j0 += 4 * 128) {
-      float x[4];
+  const int lane = tid & 31;
+  long long u = blockIdx.x;  // this CTA's next unit, counted from the request's first
+  for (int b0 = 0; b0 < P.B; b0 += 32) {
+    int ctx = 0;
+    if (b0 + lane < P.B) {
+      const TreeReq r = tree_request(P, b0 + lane);
+      if (r.ok && r.n == 0) ctx = r.ctx;
+    }
+    for (unsigned who = __ballot_sync(0xffffffffu, ctx > 0); who; who &= who - 1) {
+      const int b = b0 + __ffs(who) - 1, len = __shfl_sync(0xffffffffu, ctx, b - b0);
+      const int parts = (len + kIdle - 1) / kIdle;
+      const long long units = (long long)P.heads * parts;
+      const int32_t* table = P.table + (long long)b * P.ld_table;
+      for (; u < units; u += gridDim.x) {
+        const int h = (int)(u / parts), lo = (int)(u - (long long)h * parts) * kIdle, hi = min(len, lo + kIdle);
+        const long long at = ((long long)b * P.heads + h) * P.ld;
+        for (int j0 = lo + tid; j0 < hi; j0 += 4 * 128) {
+          float x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = j0 + i * 128;
-        x[i] = 0.f;
-        if (j >= hi) continue;
-        int page, slot;
-        pd.split(j, page, slot);
-        const int id = table[page];
-        if (before) x[i] = before[row * P.ld + j];
-        if (id < 0 || id >= P.num_pages) x[i] = NAN;
+          for (int i = 0; i < 4; ++i) {
+            const int j = j0 + i * 128;
+            x[i] = 0.f;
+            if (j >= hi) continue;
+            int page, slot;
+            pd.split(j, page, slot);
+            const int id = table[page];
+            if (before) x[i] = before[at + j];
+            if (id < 0 || id >= P.num_pages) x[i] = NAN;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (j0 + i * 128 < hi) out[at + j0 + i * 128] = x[i];
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (j0 + i * 128 < hi) out[row * P.ld + j0 + i * 128] = x[i];
+      u -= units;
     }
   }
 }
