@@ -333,3 +333,8 @@ from .tree import (  # noqa: E402,F401  (the drafted-tree operators use the help
     make_reorder_args, make_tree_args, make_tree_workspace, make_weigh_args, spec_attention_weights,
     spec_beam_reorder, spec_beam_select, spec_beam_workspace_bytes, spec_cache_commit, spec_cache_evict,
     spec_tree_attention, spec_tree_workspace_bytes)
+from .serve import (  # noqa: E402,F401
+    EXPORTED_SERVE, SpecCache8, SpecCache8Args, SpecCache8CommitArgs, SpecRotateArgs, SpecWindowArgs, make_cache8,
+    make_cache8_args, make_cache8_commit_args, make_cache8_workspace, make_rotate_args, make_window_args,
+    make_window_workspace, spec_cache8_attention, spec_cache8_commit, spec_cache8_workspace_bytes, spec_norm_rotate,
+    spec_window_attention, spec_window_workspace_bytes)

@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["spec_verify.cu", "sample_verify.cu", "pipe_verify.cu", "seg_verify.cu", "greedy_verify.cu", "confidence.cu",
-           "topp_verify.cu", "tree_ops.cu", "tree_attn.cu", "tree_tc.cu", "weigh.cu", "weigh_tc.cu", "cache_ops.cu", "beam.cu"]
+           "topp_verify.cu", "tree_ops.cu", "tree_attn.cu", "tree_tc.cu", "weigh.cu", "weigh_tc.cu", "cache_ops.cu", "beam.cu",
+           "serve_ops.cu", "norm_rotate.cu", "window_attn.cu", "window_tc.cu", "cache8_warp.cu", "cache8_ops.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 
@@ -40,7 +41,7 @@ def _stale(target: str, deps) -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    headers += [os.path.join(INCLUDE, f) for f in ("spec_verify.h", "spec_tree.h")]
+    headers += [os.path.join(INCLUDE, f) for f in ("spec_verify.h", "spec_tree.h", "spec_serve.h")]
     objs, procs = [], []
     t0 = time.time()
     for src in SOURCES:

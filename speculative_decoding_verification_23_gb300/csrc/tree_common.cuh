@@ -54,8 +54,13 @@ struct TreeReq {
   int mb;             // row blocks per head
   bool ok;
   long long tiles;    // of all items
+  // with a window: cached tokens [0, sk) and [b1, ctx) have tiles, the first st
+  // of them for the sinks; from `part` on every row sees all of the second run
+  int sk, st, b1, part;
 };
 
+// WIN: rows see a window and sinks (P.window, P.sinks, P.align).
+template <bool WIN = false>
 __device__ __forceinline__ TreeReq tree_request(const TreeParams& P, int b) {
   TreeReq r;
   r.cu = P.cu[b];
@@ -67,6 +72,16 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& P, int b) {
   // unsigned and by shifts: every role of a CTA does this before it begins
   const int kt_shift = 31 - __clz(P.kt);  // a power of two
   r.ct = (int)(((uint32_t)r.ctx + (uint32_t)P.kt - 1u) >> kt_shift);
+  if (WIN) {
+    // No row sees fewer than none of the drafted tokens, so none looks further
+    // back than `window` cached ones.
+    r.sk = min(P.sinks, r.ctx);
+    r.b1 = max(0, r.ctx - P.window) & ~(P.align - 1);
+    r.st = (int)(((uint32_t)r.sk + (uint32_t)P.kt - 1u) >> kt_shift);
+    if (r.b1 <= r.sk) r.b1 = r.st = 0;  // one run
+    r.ct = r.st + (int)(((uint32_t)(r.ctx - r.b1) + (uint32_t)P.kt - 1u) >> kt_shift);
+    r.part = r.ctx + r.n - P.window;
+  }
   r.per_item = r.ct + (int)(((uint32_t)r.n + (uint32_t)P.kt - 1u) >> kt_shift);
   r.mb = (int)((uint32_t)(r.n * P.group + P.rows - 1) / (uint32_t)P.rows);
   if (P.weigh) {
@@ -85,13 +100,14 @@ struct TreeScan {
   bool idle;  // this lane has a request of cached tokens without rows
 };
 
+template <bool WIN = false>
 __device__ __forceinline__ TreeScan tree_scan(const TreeParams& P, int lane) {
   TreeScan s;
   s.per = (P.B + 31) / 32;
   s.mine = 0;
   s.idle = false;
   for (int b = lane * s.per; b < min(P.B, (lane + 1) * s.per); ++b) {
-    const TreeReq r = tree_request(P, b);
+    const TreeReq r = tree_request<WIN>(P, b);
     s.mine += r.tiles;
     s.idle = s.idle || (r.ok && r.n == 0 && r.ctx > 0);
   }
@@ -107,6 +123,7 @@ __device__ __forceinline__ TreeScan tree_scan(const TreeParams& P, int lane) {
 }
 
 // The request that holds tile x (x < total) and its first tile.
+template <bool WIN = false>
 __device__ __forceinline__ int tree_locate(const TreeParams& P, const TreeScan& s, int lane, long long x,
                                            long long* first) {
   const bool me = x >= s.before && x < s.before + s.mine;
@@ -114,7 +131,7 @@ __device__ __forceinline__ int tree_locate(const TreeParams& P, const TreeScan& 
   long long rs = s.before;
   if (me) {
     for (rb = lane * s.per;; ++rb) {
-      const long long t = tree_request(P, rb).tiles;
+      const long long t = tree_request<WIN>(P, rb).tiles;
       if (x < rs + t) break;
       rs += t;
     }
@@ -125,11 +142,12 @@ __device__ __forceinline__ int tree_locate(const TreeParams& P, const TreeScan& 
 }
 
 // The first tile of each request, for the kernel that joins split items.
+template <bool WIN = false>
 __device__ __forceinline__ void tree_store_starts(const TreeParams& P, const TreeScan& s, int lane) {
   long long at = s.before;
   for (int b = lane * s.per; b < min(P.B, (lane + 1) * s.per); ++b) {
     P.start[b] = at;
-    at += tree_request(P, b).tiles;
+    at += tree_request<WIN>(P, b).tiles;
   }
   if (lane == 0) P.start[P.B] = s.total;
 }
@@ -154,7 +172,8 @@ struct TreeSeg {
 };
 
 // Walks a CTA's range segment by segment; every warp walks by itself.
-struct TreeWalk {
+template <bool WIN>
+struct TreeWalkOf {
   long long x, end, first;
   TreeReq r;
   int b;
@@ -165,15 +184,15 @@ struct TreeWalk {
     b = 0;
     first = 0;
     if (x < end) {
-      b = tree_locate(P, s, lane, x, &first);
-      r = tree_request(P, b);
+      b = tree_locate<WIN>(P, s, lane, x, &first);
+      r = tree_request<WIN>(P, b);
     }
   }
   __device__ __forceinline__ bool next(const TreeParams& P, TreeSeg& g) {
     if (x >= end) return false;
     while (x >= first + r.tiles) {  // ends: some request holds tile x < total
       first += r.tiles;
-      r = tree_request(P, ++b);
+      r = tree_request<WIN>(P, ++b);
     }
     const long long off = x - first;
     const int item = (int)div_fast(off, r.per_item);
@@ -186,6 +205,31 @@ struct TreeWalk {
     return true;
   }
 };
+
+using TreeWalk = TreeWalkOf<false>;
+
+// The keys of a tile: drafted or cached, the first of them, and the end of the
+// run that it is part of.
+struct TreeKeys {
+  bool cached;
+  int lo, lim;
+};
+template <bool WIN>
+__device__ __forceinline__ TreeKeys tree_keys(const TreeReq& r, int kt, int t) {
+  TreeKeys k;
+  k.cached = t < r.ct;
+  if (!k.cached) {
+    k.lo = (t - r.ct) * kt;
+    k.lim = r.n;
+  } else if (WIN && t >= r.st) {
+    k.lo = r.b1 + (t - r.st) * kt;
+    k.lim = r.ctx;
+  } else {
+    k.lo = t * kt;
+    k.lim = WIN ? r.sk : r.ctx;
+  }
+  return k;
+}
 
 // Slot of a CTA's partial result: 0 where the item began in an earlier CTA.
 __device__ __forceinline__ int tree_slot(bool item_begins_here) { return item_begins_here ? 1 : 0; }
@@ -204,6 +248,55 @@ __device__ __forceinline__ uint32_t tree_bits16(const TreeParams& P, int cu, int
   }
   const int left = n - base;
   return left >= 16 ? (bits & 0xffffu) : (left <= 0 ? 0u : bits & ((1u << left) - 1u));
+}
+
+// How many drafted tokens node `i` of a tree of n nodes sees.
+__device__ __forceinline__ int tree_seen(const TreeParams& P, int cu, int n, int i) {
+  if (!P.mask) return i + 1;
+  int seen = 0;
+  for (int w = 0; w * 32 < n; ++w) {
+    const int left = n - w * 32;
+    uint32_t x = P.mask[(long long)(cu + i) * P.mask_words + w];
+    if (left < 32) x &= (1u << left) - 1u;
+    seen += __popc(x);
+  }
+  return seen;
+}
+
+// A windowed row: it sees cached token j where j < sinks or j >= lo.
+struct TreeRow {
+  int seen;  // drafted tokens that it would see
+  int lo;
+};
+__device__ __forceinline__ TreeRow tree_row(const TreeParams& P, const TreeReq& r, int node) {
+  TreeRow w;
+  w.seen = r.part > 0 ? tree_seen(P, r.cu, r.n, node) : 0;  // nothing is hidden where the window holds all
+  w.lo = r.part > 0 ? r.ctx + w.seen - P.window : 0;
+  return w;
+}
+
+// Which of the 32 cached tokens from `base` on a windowed row sees.
+__device__ __forceinline__ uint32_t tree_window32(int base, int lo, int sinks) {
+  const int a = lo - base, s = sinks - base;
+  const uint32_t late = a <= 0 ? 0xffffffffu : (a >= 32 ? 0u : 0xffffffffu << a);
+  const uint32_t first = s >= 32 ? 0xffffffffu : (s <= 0 ? 0u : (1u << s) - 1u);
+  return late | first;
+}
+
+// `bits`: which of the drafted tokens from `base` on a row would see.  Without
+// those that its window hides: its own text is the cached tokens and, after
+// them, the drafted ones that it sees, so it hides only where these alone
+// outnumber the window.
+__device__ __forceinline__ uint32_t tree_window_drafted(const TreeParams& P, const TreeReq& r, const TreeRow& w, int node,
+                                                        int base, uint32_t bits) {
+  if (w.seen <= P.window || bits == 0u) return bits;
+  // places 0 .. w.seen - 1 among the seen ones: [from, to) are hidden
+  const int from = max(0, P.sinks - r.ctx), to = w.seen - P.window;
+  int place = base <= 0 ? 0 : (P.mask ? tree_seen(P, r.cu, min(r.n, base), node) : min(base, node + 1));
+  uint32_t out = 0u;
+  for (uint32_t left = bits; left; left &= left - 1u, ++place)
+    if (place < from || place >= to) out |= left & (0u - left);
+  return out;
 }
 
 // Division of a token's position by the page size: a shift where it is a

@@ -44,6 +44,9 @@ struct TreeParams {
   int weigh;       // the rows are the last of the cached tokens: no drafted keys, all rows in one block,
                    // and a request has at most `ld` tokens
   int ld;
+  int window;      // a row sees the last `window` and the first `sinks` of the tokens that it would see;
+  int sinks;       // read by the windowed kernels alone
+  int align;       // the windows' first tile begins at a multiple of this (a power of two that divides the page size)
 };
 
 struct TreeWorkspace {
