@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["spec_verify.cu", "sample_verify.cu", "pipe_verify.cu", "seg_verify.cu", "greedy_verify.cu", "confidence.cu",
            "topp_verify.cu", "tree_ops.cu", "tree_attn.cu", "tree_tc.cu", "weigh.cu", "weigh_tc.cu", "cache_ops.cu", "beam.cu",
-           "serve_ops.cu", "norm_rotate.cu", "window_attn.cu", "window_tc.cu", "cache8_warp.cu", "cache8_ops.cu"]
+           "serve_ops.cu", "norm_rotate.cu", "window_attn.cu", "window_tc.cu", "cache8_warp.cu", "cache8_tc.cu", "cache8_ops.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

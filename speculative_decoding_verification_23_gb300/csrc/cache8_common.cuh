@@ -25,6 +25,13 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
   return r;
 }
 
+// The larger of each of two 16-bit whole numbers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // The sizes of two 16-bit values, infinities and NaN as 0.
 __device__ __forceinline__ uint32_t finite_size2(uint32_t two, uint32_t em) {
   const uint32_t lo = two & 0x7fffu, hi = (two >> 16) & 0x7fffu;

@@ -91,8 +91,8 @@ __global__ void __launch_bounds__(kW8Warps * 32, W8Shape<D>::kCtas) cache8_warp_
 #pragma unroll
       for (int i = 0; i < B32; ++i) {
         v[i] = in ? load16(src + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(finite_size2(v[i].x, em), finite_size2(v[i].y, em)),
-                                     __vmaxu2(finite_size2(v[i].z, em), finite_size2(v[i].w, em))));
+        top = max_u16x2(top, max_u16x2(max_u16x2(finite_size2(v[i].x, em), finite_size2(v[i].y, em)),
+                                     max_u16x2(finite_size2(v[i].z, em), finite_size2(v[i].w, em))));
       }
       top = max(top & 0xffffu, top >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -208,15 +208,15 @@ __global__ void __launch_bounds__(kW8Warps * 32, W8Shape<D>::kCtas) cache8_warp_
           const uint4 x[2] = {load16(k0 + 32 * i), load16(k1 + 32 * i)};
 #pragma unroll
           for (int z = 0; z < 2; ++z)
-            kt = __vmaxu2(kt, __vmaxu2(__vmaxu2(finite_size2(x[z].x, em), finite_size2(x[z].y, em)),
-                                       __vmaxu2(finite_size2(x[z].z, em), finite_size2(x[z].w, em))));
+            kt = max_u16x2(kt, max_u16x2(max_u16x2(finite_size2(x[z].x, em), finite_size2(x[z].y, em)),
+                                       max_u16x2(finite_size2(x[z].z, em), finite_size2(x[z].w, em))));
           const uint4 y[2] = {load16(v0 + 32 * i), load16(v1 + 32 * i)};
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
             const uint32_t w[4] = {y[z].x, y[z].y, y[z].z, y[z].w};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              vt = __vmaxu2(vt, finite_size2(w[c], em));
+              vt = max_u16x2(vt, finite_size2(w[c], em));
               odd |= (uint32_t)((w[c] & em) == em || ((w[c] >> 16) & em) == em);
             }
           }

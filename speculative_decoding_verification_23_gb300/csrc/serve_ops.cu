@@ -11,7 +11,10 @@ int launch_window_tc(const TreeParams& P, bool bf16, cudaStream_t s);
 int launch_window_join(const TreeParams& P, bool bf16, int num_sms, cudaStream_t s);
 TreePlan plan_cache8_warp(int dim, int num_sms);
 int launch_cache8_warp(const Cache8Params& C, bool bf16, cudaStream_t s);
-int launch_commit8(Commit8Params& P, bool bf16, cudaStream_t s);
+bool cache8_tc_fits(int dim, int page_size, int block);
+TreePlan plan_cache8_tc(int rows, int num_sms);
+int launch_cache8_tc(const Cache8Params& C, bool bf16, cudaStream_t s);
+int launch_commit8(Commit8Params& P, bool bf16, int num_sms, cudaStream_t s);
 }  // namespace sv
 
 namespace {
@@ -114,7 +117,17 @@ int check_cache8_args(const spec_cache8_args* a, spec_tree_args* t) {
   return a->window == 0 && a->sinks == 0 ? SPEC_OK : check_window(a->window, a->sinks);
 }
 
-sv::TreePlan plan_cache8(const spec_cache8_args* a, int num_sms) { return sv::plan_cache8_warp(a->cache.dim, num_sms); }
+// The tensor-memory kernel takes the calls whose tiles TMA can copy, with more
+// query rows per key head than one warp tile holds.
+constexpr int kWarpRows8 = 16;
+
+sv::TreePlan plan_cache8(const spec_cache8_args* a, int num_sms) {
+  const spec_cache8& c = a->cache;
+  const int rows = a->max_nodes * (a->heads_q / c.heads);
+  const bool fits = rows <= kMaxTcRows && sv::cache8_tc_fits(c.dim, c.page_size, c.block) && a->total_nodes > 0 &&
+                    tma_stride(c.s_slot, c.page_size) && tma_stride(c.s_head, c.heads) && tma_stride(c.s_page, c.num_pages);
+  return fits && rows > kWarpRows8 ? sv::plan_cache8_tc(rows, num_sms) : sv::plan_cache8_warp(c.dim, num_sms);
+}
 
 // The largest power of two up to 64 that divides the page size: the copies of
 // the tensor-memory kernels hold this many tokens, and warp tiles begin
@@ -260,7 +273,7 @@ int spec_cache8_attention(const spec_cache8_args* a, void* out, int64_t so_node,
   C.block = a->cache.block;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = a->dtype == SPEC_BF16;
-  if (sv::launch_cache8_warp(C, bf16, s)) return SPEC_ERR_LAUNCH;
+  if (plan.kernel == 1 ? sv::launch_cache8_tc(C, bf16, s) : sv::launch_cache8_warp(C, bf16, s)) return SPEC_ERR_LAUNCH;
   return sv::launch_window_join(C.t, bf16, sms, s) == 0 ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 
@@ -327,8 +340,7 @@ int spec_cache8_commit(const spec_cache8_commit_args* a, int32_t* out_len, int32
   P.heads = c.heads;
   P.dim = c.dim;
   P.block = c.block;
-  return sv::launch_commit8(P, a->dtype == SPEC_BF16, reinterpret_cast<cudaStream_t>(stream)) == 0 ? SPEC_OK
-                                                                                                   : SPEC_ERR_LAUNCH;
+  return sv::launch_commit8(P, a->dtype == SPEC_BF16, sms, reinterpret_cast<cudaStream_t>(stream)) == 0 ? SPEC_OK : SPEC_ERR_LAUNCH;
 }
 
 }  // extern "C"

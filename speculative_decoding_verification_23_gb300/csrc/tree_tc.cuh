@@ -78,9 +78,11 @@ __device__ __forceinline__ uint32_t tc_sees(const TreeParams& P, const TreeReq& 
 // Adds the infinities and NaN among the values of a segment's tiles that some
 // rows see and others do not, where this row sees them, to its result, which
 // was computed with zeros in their places: to the written row `dst`, or to its
-// partial result (unnormalised: the weight's size does not matter).
+// partial result (unnormalised: the weight's size does not matter).  By value:
+// the walk's state would live in local memory, which has little of the
+// first-level cache beside this much shared memory.
 template <typename T, int D, bool WIN>
-__device__ __noinline__ void add_odd(const TreeParams& P, const TreeReq& r, const TreeRow& win, int node, const TreeSeg& g,
+__device__ __noinline__ void add_odd(const TreeParams& P, const TreeReq r, const TreeRow win, int node, const TreeSeg g,
                                      T* dst, float4* part) {
   const uint32_t em = exp_mask<T>();
   const PageDiv pd(P.page_size);

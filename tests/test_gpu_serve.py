@@ -338,6 +338,40 @@ def test_a_long_context_is_split(block):
     c.check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group,nodes", [(128, 4, 64), (64, 8, 40), (128, 2, 30)])
+def test_many_tiles_over_8_bits(dtype, dim, group, nodes):
+    """Dozens of tiles of each CTA, of many segments: as the 16-bit kernel over the same values, up to the rounding of
+    weights in both (half a step relative to what they add up, and of the result) and of the keys and values to bf16
+    (exact: e4m3 with scales of powers of two)."""
+    g, rng, t = gen(3), np.random.RandomState(3), DT[dtype]
+    kv, page, B = 8, 16, 12
+    ctx = rng.randint(1000, 9000, B).tolist()
+    need = [-(-c // page) for c in ctx]
+    table = np.zeros((B, max(need)), np.int32)
+    ids, at = rng.permutation(sum(need)), 0
+    for b, n in enumerate(need):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    shape = (sum(need), page, kv, dim)
+    k8, v8 = ((torch.randn(shape, generator=g, device=DEV) * 64).clamp(-448, 448).to(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (2.0 ** torch.randint(-7, -4, (sum(need), 1, kv), generator=g, device=DEV) for _ in range(2))
+    q = normal(g, B * nodes, kv * group, dim, dtype=t, scale=0.7)
+    k_new, v_new = normal(g, B * nodes, kv, dim, dtype=t), normal(g, B * nodes, kv, dim, dtype=t)
+    m = torch.from_numpy(trees(rng, [nodes] * B, -(-nodes // 32)).view(np.int32)).to(DEV)
+    a = dict(q=q, k_new=k_new, v_new=v_new, cu_nodes=i32(np.arange(B + 1) * nodes), max_nodes=nodes, block_table=i32(table),
+             ctx_len=i32(ctx), tree_mask=m)
+    out, lse, status = sv.spec_cache8_attention(sv.make_cache8_args(cache=sv.make_cache8(k8, v8, ks, vs), **a))
+    k16, v16 = ((x.float() * s[..., None]).to(t) for x, s in ((k8, ks), (v8, vs)))
+    want, w_lse, _ = sv.spec_tree_attention(sv.make_tree_args(cache=sv.make_cache(k16, v16), **a))
+    assert status.tolist() == [0] * B
+    # softmax weights over at least 1000 keys of values up to 14 in size
+    assert (lse - w_lse).abs().max() <= 1e-4
+    assert (out.float() - want.float()).abs().max() <= (2 * 2.0 ** -8 + 2.0 ** -10 if dtype == "bf16" else 4 * 2.0 ** -11) * 2.0
+    again = sv.spec_cache8_attention(sv.make_cache8_args(cache=sv.make_cache8(k8, v8, ks, vs), **a))
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
 def test_few_requests_rows_and_layers_of_an_8_bit_cache():
     """Layers, a cache of other strides, outputs of other strides; a request without nodes."""
     g = gen(1)
