@@ -33,6 +33,12 @@ constexpr int kC8Tiles = 8;        // tiles that are described ahead
 constexpr int kC8Segs = 16;        // segments: more than may be described beside one that is still being written
 constexpr int kC8Softmax = 8, kC8Convert = 4;       // warps, then two that copy and two that issue products
 constexpr int kC8TcThreads = 32 * (kC8Softmax + kC8Convert + 4);
+// Whether values of T need a scale to be exact in fp16.
+template <typename T>
+constexpr bool kScaled = true;
+template <>
+constexpr bool kScaled<__half> = false;
+
 // Two columns of this warp's 32 lanes, with the wait.
 __device__ __forceinline__ void tmem_st2(uint32_t addr, float a, float b) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(addr),
@@ -365,12 +371,12 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
         }
       }
     };
-    Batch a, b;
+    // The next four are looked up before these are copied.
+    Batch a;
     look(a);
-    while (ok && a.count > 0) {  // the next four are looked up before these are copied
-      look(b);
-      issue(a);
-      if (!ok || b.count == 0) break;
+#pragma unroll 1
+    while (ok && a.count > 0) {
+      const Batch b = a;
       look(a);
       issue(b);
     }
@@ -441,48 +447,46 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
         if (ok) scores(n16, 0);
         if (PAIR && ok && n16 > kUnit8) scores(n16, 1);
       }
-      for (int i = first; ok && i < left; i += STEP) {
-        const int next = i + STEP < left ? tile_keys(tc + i + STEP) : 0;
-        const uint64_t db = dv + (uint32_t)(v_slot * (S::kSlot >> 4));
-        ok = ok && warp_wait(&h_full[v_slot], v_ph) && warp_wait(&p_ready[w * 2], p_ph & 1);
-        if (!ok) break;
-        p_ph ^= 1u;
-        tc_fence_after();
-        if (n16 >= kUnit8) {
-#pragma unroll
-          for (int ks = 0; ks < kUnit8 / 16; ++ks)
-            mma_ts(o, p + ks * 8, db + ks * (2048 >> 4), id_v, ks > 0 || i > first, one);
-        } else {
+      int next = first + STEP < left ? tile_keys(tc + first + STEP) : 0;
 #pragma unroll 1
-          for (int ks = 0; ks < n16 / 16; ++ks) mma_ts(o, p + ks * 8, db + ks * (2048 >> 4), id_v, ks > 0 || i > first, one);
-        }
-        mma_commit(&o_half[w], one);
-        if (PAIR && next > 0) scores(next, 0);
-        if (n16 > kUnit8) {
-          ok = ok && warp_wait(&p_ready[w * 2 + 1], (p_ph >> 1) & 1);
+      for (int i = first; ok && i < left; i += STEP) {
+        ok = ok && warp_wait(&h_full[v_slot], v_ph);
+#pragma unroll 1
+        for (int h = 0; ok && h * kUnit8 < n16; ++h) {
+          ok = warp_wait(&p_ready[w * 2 + h], (p_ph >> h) & 1);
           if (!ok) break;
-          p_ph ^= 2u;
+          p_ph ^= 1u << h;
           tc_fence_after();
-          if (n16 == kTcKeys) {
+          const uint64_t db = dv + (uint32_t)(v_slot * (S::kSlot >> 4) + h * (4 * 2048 >> 4));
+          const uint32_t at = p + h * kUnit8, begun = h > 0 || i > first;
+          const int steps = min(4, n16 / 16 - h * 4);
+          if (steps == 4) {
 #pragma unroll
-            for (int ks = 4; ks < 8; ++ks) mma_ts(o, p + 32 + ks * 8, db + ks * (2048 >> 4), id_v, true, one);
+            for (int ks = 0; ks < 4; ++ks) mma_ts(o, at + ks * 8, db + ks * (2048 >> 4), id_v, ks > 0 || begun, one);
           } else {
 #pragma unroll 1
-            for (int ks = 4; ks < n16 / 16; ++ks) mma_ts(o, p + 32 + ks * 8, db + ks * (2048 >> 4), id_v, true, one);
+            for (int ks = 0; ks < steps; ++ks) mma_ts(o, at + ks * 8, db + ks * (2048 >> 4), id_v, ks > 0 || begun, one);
           }
+          if (h == 0) mma_commit(&o_half[w], one);
+          if ((h + 1) * kUnit8 >= n16) {
+            mma_commit(&o_done[w], one);  // before the scores that the softmax takes for a sign of it
+            mma_commit(&h_empty[v_slot], one);
+          }
+          if (PAIR && next > h * kUnit8) scores(next, h);
         }
-        mma_commit(&o_done[w], one);  // before the scores that the softmax takes for a sign of it
-        mma_commit(&h_empty[v_slot], one);
+        if (!ok) break;
+        // what the tile had no half for
+        if (PAIR ? n16 <= kUnit8 && next > kUnit8 : next > 0) scores(next, PAIR ? 1 : 0);
         v_slot += 2 * STEP;
         if (v_slot >= S::kSlots) {
           v_slot -= S::kSlots;
           v_ph ^= 1;
         }
-        if (PAIR ? next > kUnit8 : next > 0) scores(next, PAIR ? 1 : 0);
         if (i + STEP >= left) mma_commit(&o_last[w], one);
         leave_tile(tc + i);
         if (!PAIR && i + 1 < left) leave_tile(tc + i + 1);
         n16 = next;
+        next = i + 2 * STEP < left ? tile_keys(tc + i + 2 * STEP) : 0;
       }
       tc += left;
     }
@@ -514,11 +518,11 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
       if (cached) ok = warp_wait(&raw_full[rs], rph);
       ok = ok && warp_wait(&h_empty[slot], hph);
       if (!ok) break;
+      bool odd = false;
+      if (cached) {
 #pragma unroll 1
-      for (int row = row0; row - lane < n16; row += 64) {
-        unsigned char* dst = ring + slot * S::kSlot + row * 128;
-        bool odd = false;
-        if (cached) {
+        for (int row = row0; row - lane < n16; row += 64) {
+          unsigned char* dst = ring + slot * S::kSlot + row * 128;
           const unsigned char* src = raws + rs * S::kRaw + row * D;
           // all loads first: only what a warp has in flight by itself hides
           // latencies
@@ -553,38 +557,38 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
                 make_uint4(e4m3x2_f16x2(v[c].z & 0xffffu), e4m3x2_f16x2(v[c].z >> 16), e4m3x2_f16x2(v[c].w & 0xffffu),
                            e4m3x2_f16x2(v[c].w >> 16));
           }
-        } else {
-          const C8Seg& e = segs[seg & (kC8Segs - 1)];
-          const T* src = static_cast<const T*>(kv ? P.v_new : P.k_new) +
-                         (long long)(e.cu + x.lo + min(row, valid - 1)) * P.sn_node + (long long)e.kvh * P.sn_head;
-          uint4 v[D / 8];
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) v[c] = row < valid ? load16(src + c * 8) : make_uint4(0u, 0u, 0u, 0u);
-          uint32_t top = 0;
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            uint32_t* y = reinterpret_cast<uint32_t*>(&v[c]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              top = max_u16x2(top, finite_size2(y[k], em));
-              if (kv) {
-                if ((y[k] & em) == em) {
-                  y[k] &= 0xffff0000u;
-                  odd = true;
-                }
-                if (((y[k] >> 16) & em) == em) {
-                  y[k] &= 0xffffu;
-                  odd = true;
-                }
-              }
+        }
+      } else {
+        // 16 keys a warp at once: a lane has 8 channels of every (256 / D)-th, copied
+        // to where they belong and scaled there.  Little code, as for queries.
+        constexpr int PCS = D / 8, RS = 32 / PCS;
+        const C8Seg& e = segs[seg & (kC8Segs - 1)];
+        const int piece = lane % PCS, r0 = lane / PCS;
+        const T* base = static_cast<const T*>(kv ? P.v_new : P.k_new) + (long long)(e.cu + x.lo) * P.sn_node +
+                        (long long)e.kvh * P.sn_head + piece * 8;
+        auto place = [&](int row) {
+          return ring + slot * S::kSlot + (piece >> 3) * S::kHalf + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+        };
+#pragma unroll 1
+        for (int g = (warp & 1) * 16; g < n16; g += 32) {
+#pragma unroll 1
+          for (int row = g + r0; row < g + 16; row += RS)
+            cp_async16(smem_u32(place(row)), base + (long long)min(row, valid - 1) * P.sn_node, row < valid);
+          cp_async_commit();
+          cp_async_wait<0>();
+          Exact16 s16 = {1.f, 1.f};
+          if (kScaled<T>) {
+            uint32_t top = 0;
+#pragma unroll 1
+            for (int row = g + r0; row < g + 16; row += RS) {
+              const uint4 v = *reinterpret_cast<const uint4*>(place(row));
+              top = max_u16x2(top, max_u16x2(max_u16x2(finite_size2(v.x, em), finite_size2(v.y, em)),
+                                             max_u16x2(finite_size2(v.z, em), finite_size2(v.w, em))));
             }
+            s16 = exact16<T>(__reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)));
           }
-          top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-          for (int z = 8; z > 0; z >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, z));
-          const Exact16 s16 = exact16<T>(top);
-          if ((row & 15) == 0) {
-            float4* at = &scales[tc & (kC8Tiles - 1)][row >> 4];
+          if (lane == 0) {
+            float4* at = &scales[tc & (kC8Tiles - 1)][g >> 4];
             if (kv == 0) {
               at->x = s16.back;
             } else {
@@ -593,15 +597,31 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
               at->z = y.z;
             }
           }
-          if (row < n16)
+          if (kScaled<T> || kv) {
+#pragma unroll 1
+            for (int row = g + r0; row < g + 16; row += RS) {
+              uint4 v = *reinterpret_cast<const uint4*>(place(row));
+              uint32_t* y = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-              *reinterpret_cast<uint4*>(dst + (c >> 3) * S::kHalf + ((uint32_t)((c & 7) << 4) ^ out_x)) =
-                  make_uint4(to_f16x2<T>(v[c].x, s16.to), to_f16x2<T>(v[c].y, s16.to), to_f16x2<T>(v[c].z, s16.to),
-                             to_f16x2<T>(v[c].w, s16.to));
+              for (int z = 0; z < 4; ++z) {
+                if (kv) {  // infinities and NaN are left out
+                  if ((y[z] & em) == em) {
+                    y[z] &= 0xffff0000u;
+                    odd = true;
+                  }
+                  if (((y[z] >> 16) & em) == em) {
+                    y[z] &= 0xffffu;
+                    odd = true;
+                  }
+                }
+                y[z] = to_f16x2<T>(y[z], s16.to);
+              }
+              *reinterpret_cast<uint4*>(place(row)) = v;
+            }
+          }
         }
-        if (odd) segs[seg & (kC8Segs - 1)].odd = 1;
       }
+      if (odd) segs[seg & (kC8Segs - 1)].odd = 1;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
@@ -646,44 +666,43 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
       const C8Seg e = segs[seg & (kC8Segs - 1)];
       const int row_lo = e.m * (S::kQTiles * kRows8) + tile * kRows8;
       const int nrows = min(kRows8, e.n * P.group - row_lo);  // may be <= 0
-      // This tile's query rows in fp16, scaled to be exact there.  A thread has
-      // one 16-byte piece of every (threads / (D / 8))-th row.
-      constexpr int PER = D / 8, STEP = (PAIR ? 128 : 256) / PER, N = kRows8 / STEP < 8 ? kRows8 / STEP : 8;
+      // This tile's query rows, scaled to be exact in fp16.  A thread has one
+      // 16-byte piece of every (threads / (D / 8))-th row, copied to where it
+      // belongs and scaled there.  Little code: it is read anew for every segment.
+      constexpr int PER = D / 8, STEP = (PAIR ? 128 : 256) / PER;
       const int ch = wtid % PER;
-      const T* src = static_cast<const T*>(P.q) + (long long)e.cu * P.sq_node + ch * 8;
+      const T* src = static_cast<const T*>(P.q) + (long long)e.cu * P.sq_node + (long long)(e.kvh * P.group) * P.sq_head + ch * 8;
+      auto place = [&](int rr) { return qs + (ch >> 3) * (kRows8 * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4); };
 #pragma unroll 1
-      for (int r0 = wtid / PER; r0 < kRows8; r0 += N * STEP) {
-        uint4 v[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int rr = r0 + i * STEP, R = row_lo + rr;
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (rr < nrows) {
-            const int nd = (int)(((float)R + 0.5f) * inv_group);
-            v[i] = load16(src + (long long)nd * P.sq_node + (long long)(e.kvh * P.group + R - nd * P.group) * P.sq_head);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int rr = r0 + i * STEP;
-          uint32_t top = max_u16x2(max_u16x2(finite_size2(v[i].x, em), finite_size2(v[i].y, em)),
-                                  max_u16x2(finite_size2(v[i].z, em), finite_size2(v[i].w, em)));
+      for (int rr = wtid / PER; rr < kRows8; rr += STEP) {
+        const int R = row_lo + min(rr, max(nrows - 1, 0)), nd = (int)(((float)R + 0.5f) * inv_group);
+        cp_async16(smem_u32(place(rr)), src + (long long)nd * P.sq_node + (long long)(R - nd * P.group) * P.sq_head, rr < nrows);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      if (kScaled<T>) {
+#pragma unroll 1
+        for (int rr = wtid / PER; rr < nrows; rr += STEP) {
+          uint4 v = *reinterpret_cast<const uint4*>(place(rr));
+          uint32_t top = max_u16x2(max_u16x2(finite_size2(v.x, em), finite_size2(v.y, em)),
+                                   max_u16x2(finite_size2(v.z, em), finite_size2(v.w, em)));
           top = max(top & 0xffffu, top >> 16);
+          const uint32_t peers = __activemask();
 #pragma unroll
-          for (int z = PER / 2; z > 0; z >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, z));
+          for (int z = PER / 2; z > 0; z >>= 1) top = max(top, __shfl_xor_sync(peers, top, z));
           const Exact16 s16 = exact16<T>(top);
           if (ch == 0) row_scale[tile][rr] = (uint8_t)((__float_as_uint(s16.back) >> 23) - 63);
-          *reinterpret_cast<uint4*>(qs + (ch >> 3) * (kRows8 * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) =
-              make_uint4(to_f16x2<T>(v[i].x, s16.to), to_f16x2<T>(v[i].y, s16.to), to_f16x2<T>(v[i].z, s16.to),
-                         to_f16x2<T>(v[i].w, s16.to));
+          *reinterpret_cast<uint4*>(place(rr)) =
+              make_uint4(to_f16x2<T>(v.x, s16.to), to_f16x2<T>(v.y, s16.to), to_f16x2<T>(v.z, s16.to), to_f16x2<T>(v.w, s16.to));
         }
+        __syncwarp();
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(&q_full[tile]);
       ok = warp_wait(&q_full[tile], seg & 1);  // the rows' scales
       if (!ok) break;
-      const float rsc = P.scale_log2 * __uint_as_float((uint32_t)(row_scale[tile][row] + 63) << 23);
       const bool mine = row < nrows;
+      const float rsc = !mine ? 0.f : kScaled<T> ? P.scale_log2 * __uint_as_float((uint32_t)(row_scale[tile][row] + 63) << 23) : P.scale_log2;
       const bool any = (warp & 3) * 32 < nrows;  // warp-uniform
       const int R = row_lo + (mine ? row : 0);
       const int node = mine ? (int)(((float)R + 0.5f) * inv_group) : 0;
@@ -700,9 +719,13 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
       for (int i = first; ok && i < left; i += TSTEP, ++mine_tc) {
         const int at = (tc + i) & (kC8Tiles - 1);
         // also says that the tile is described
-        ok = warp_wait(&sc_full[at], ((tc + i) / kC8Tiles) & 1);
+        ok = wait_tile(tc + i);
         if (!ok) break;
         const C8Desc x = tiles[at];
+        if (!x.cached()) {
+          ok = warp_wait(&sc_full[at], ((tc + i) / kC8Tiles) & 1);
+          if (!ok) break;
+        }
         const int valid = x.valid(), n16 = x.n16();
         const bool masked = valid < kTcKeys || x.some();
 #pragma unroll 1

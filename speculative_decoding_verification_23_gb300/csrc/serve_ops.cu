@@ -117,14 +117,14 @@ int check_cache8_args(const spec_cache8_args* a, spec_tree_args* t) {
   return a->window == 0 && a->sinks == 0 ? SPEC_OK : check_window(a->window, a->sinks);
 }
 
-// The tensor-memory kernel takes the calls whose tiles TMA can copy, with more
-// query rows per key head than one warp tile holds.
+// The tensor-memory kernel takes the calls whose tiles TMA can copy, with a
+// positive scale, and more query rows per key head than one warp tile holds.
 constexpr int kWarpRows8 = 16;
 
 sv::TreePlan plan_cache8(const spec_cache8_args* a, int num_sms) {
   const spec_cache8& c = a->cache;
   const int rows = a->max_nodes * (a->heads_q / c.heads);
-  const bool fits = rows <= kMaxTcRows && sv::cache8_tc_fits(c.dim, c.page_size, c.block) && a->total_nodes > 0 &&
+  const bool fits = rows <= kMaxTcRows && a->scale > 0.f && sv::cache8_tc_fits(c.dim, c.page_size, c.block) && a->total_nodes > 0 &&
                     tma_stride(c.s_slot, c.page_size) && tma_stride(c.s_head, c.heads) && tma_stride(c.s_page, c.num_pages);
   return fits && rows > kWarpRows8 ? sv::plan_cache8_tc(rows, num_sms) : sv::plan_cache8_warp(c.dim, num_sms);
 }
