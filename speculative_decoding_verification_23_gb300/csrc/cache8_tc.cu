@@ -217,11 +217,11 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
     for (int i = 0; i < kC8Tiles; ++i) {
       mbar_init(&d_full[i], 1);
       mbar_init(&sc_full[i], 1 + kC8Convert);
-      mbar_init(&d_empty[i], kC8Softmax + kC8Convert + 2);
+      mbar_init(&d_empty[i], kC8Convert + 2);  // the products' warps leave a tile when its softmax has ended
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_ready[i], 128);
+      mbar_init(&p_ready[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], PAIR ? 128 : 256);
@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
   const uint32_t tmem = uniform(tmem_at);
   int tc = 0;  // tiles so far: the rings hold keys of tile i as fill 2i, values as 2i + 1
 
-  // The description of tile i; everyone reads it, or passes it by, before it is
-  // written over.
+  // The description of tile i; the conversion and the products' warps read it, or
+  // pass it by, before it is written over.
   auto wait_tile = [&](int i) { return warp_wait(&d_full[i & (kC8Tiles - 1)], (i / kC8Tiles) & 1); };
   auto leave_tile = [&](int i) {
     __syncwarp();
@@ -715,19 +715,45 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
       float2 l2 = make_float2(0.f, 0.f), l3 = l2;  // its sum
       constexpr int TSTEP = PAIR ? 1 : 2;
       const int first = PAIR ? 0 : (tc ^ w) & 1;
-      if (!PAIR && first == 1) leave_tile(tc);
       for (int i = first; ok && i < left; i += TSTEP, ++mine_tc) {
         const int at = (tc + i) & (kC8Tiles - 1);
         // also says that the tile is described
         ok = wait_tile(tc + i);
         if (!ok) break;
         const C8Desc x = tiles[at];
+        const int valid = x.valid(), n16 = x.n16();
+        const bool masked = valid < kTcKeys || x.some();
+        uint32_t see[4];
+        if (x.some() && any) {
+          if (x.cached()) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) see[c] = tree_window32(x.lo + c * 32, see_lo, P.sinks);
+          } else {
+            // all words at once; x.lo is a multiple of 32
+            const uint32_t* words = P.mask + (long long)(e.cu + node) * P.mask_words;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int wd = (x.lo >> 5) + c, k = node - x.lo - c * 32;
+              see[c] = P.mask ? (wd < P.mask_words ? words[wd] : 0u) : k < 0 ? 0u : k >= 31 ? 0xffffffffu : (2u << k) - 1u;
+            }
+            if (seen > P.window) {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t left = c8_sees(P, e.cu, e.n, e.ctx, seen, see_lo, node, false, x.lo + c * 32);
+                see[0] = c == 0 ? left : see[0];
+                see[1] = c == 1 ? left : see[1];
+                see[2] = c == 2 ? left : see[2];
+                see[3] = c == 3 ? left : see[3];
+              }
+            }
+          }
+        }
+        // cached keys' scales come with the description; the conversion, which
+        // knows drafted ones', may still be waiting for room
         if (!x.cached()) {
           ok = warp_wait(&sc_full[at], ((tc + i) / kC8Tiles) & 1);
           if (!ok) break;
         }
-        const int valid = x.valid(), n16 = x.n16();
-        const bool masked = valid < kTcKeys || x.some();
 #pragma unroll 1
         for (int h = 0; h * kUnit8 < n16; ++h) {
           uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
@@ -736,8 +762,7 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
             for (int c = 0; c < 2; ++c) {
               const int rest = valid - h * kUnit8 - c * 32;
               bits[c] = rest >= 32 ? 0xffffffffu : (rest <= 0 ? 0u : (1u << rest) - 1u);
-              if (x.some())
-                bits[c] &= c8_sees(P, e.cu, e.n, e.ctx, seen, see_lo, node, x.cached(), x.lo + h * kUnit8 + c * 32);
+              if (x.some()) bits[c] &= h == 0 ? see[c] : see[2 + c];
             }
           }
           if (PAIR || h == 0) {
@@ -831,10 +856,9 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
             tc_wait_st();
           }
           tc_fence_before();
-          mbar_arrive(&p_ready[w * 2 + h]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[w * 2 + h]);
         }
-        leave_tile(tc + i);
-        if (!PAIR && i + 1 < left) leave_tile(tc + i + 1);
       }
       if (!ok) break;
       const bool had = first < left;  // this stream's part in the segment
@@ -886,36 +910,28 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
       constexpr int CH = PAIR ? D : D / 2;
       const int c0 = PAIR ? 0 : w * CH;
 #pragma unroll 1
-      for (int c = 0; c < CH / 32; ++c) {
-        float o[32];
+      for (int c = c0; c < c0 + CH; c += 16) {
+        uint32_t o[16];
         __syncwarp();
-        tmem_ld32(at0 + c0 + c * 32, o);
-        tmem_wait_ld();
-        loaded(o);
+        tmem_ld16(at0 + c, o);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] *= g0;
+        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * g0);
         if (!PAIR && two) {
-          float o1[32];
-          tmem_ld32(at0 + D + c0 + c * 32, o1);
-          tmem_wait_ld();
-          loaded(o1);
+          uint32_t o1[16];
+          tmem_ld16(at0 + D + c, o1);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = fmaf(o1[k], g1, o[k]);
+          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(fmaf(__uint_as_float(o1[k]), g1, __uint_as_float(o[k])));
         }
         if (mine && whole) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            uint4 v;
-            v.x = pack2<T>(o[k], o[k + 1]);
-            v.y = pack2<T>(o[k + 2], o[k + 3]);
-            v.z = pack2<T>(o[k + 4], o[k + 5]);
-            v.w = pack2<T>(o[k + 6], o[k + 7]);
-            *reinterpret_cast<uint4*>(dst + c0 + c * 32 + k) = v;
-          }
+          for (int k = 0; k < 16; k += 8)
+            *reinterpret_cast<uint4*>(dst + c + k) =
+                make_uint4(pack2<T>(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), pack2<T>(__uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])),
+                           pack2<T>(__uint_as_float(o[k + 4]), __uint_as_float(o[k + 5])), pack2<T>(__uint_as_float(o[k + 6]), __uint_as_float(o[k + 7])));
         } else if (mine) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            part[((c0 + c * 32 + k) / 4) * P.rows] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          for (int k = 0; k < 16; k += 4)
+            *reinterpret_cast<uint4*>(&part[((c + k) / 4) * P.rows]) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
         }
       }
       if (mine) {
