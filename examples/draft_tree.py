@@ -102,6 +102,32 @@ def grow(model, last, ctx, beams, depth):
             1 + (depth - 1) * beams)
 
 
+def agree(model, logits, tokens, depths, parents, leaf):
+    """The longest branch of each tree that agrees with the target: its nodes [B, depth + 1], how many of them to commit
+    [B], and the target's tokens after them."""
+    B, n = tokens.shape
+    # every branch from the root to a leaf, verified as a chain of drafts
+    leaves = torch.arange(leaf, n, device=DEV).expand(B, -1)
+    branch = [leaves]
+    for _ in range(int(depths[-1])):
+        branch.append(torch.gather(parents, 1, branch[-1]))
+    branch = torch.stack(branch[::-1], 2)                     # [B, leaves, depth + 1] nodes
+    L, D = branch.shape[1], branch.shape[2] - 1
+    rows = logits.view(B, n, -1)[torch.arange(B, device=DEV)[:, None, None], branch].flatten(0, 2).contiguous()
+    path_tokens = torch.gather(tokens, 1, branch.flatten(1)).view(B, L, D + 1).int()
+    cu_draft = torch.arange(0, B * L * D + 1, D, dtype=torch.int32, device=DEV) if D else torch.zeros(
+        B * L + 1, dtype=torch.int32, device=DEV)
+    proposed = path_tokens[:, :, 1:].reshape(-1).contiguous()     # held: this argument block keeps no tensor
+    out, accepted, status = sv.spec_verify_greedy(
+        sv.make_args(target=rows, cu_draft=cu_draft, draft_tokens=proposed, V=model.vocab, max_k=D))
+    assert int(status.abs().max()) == 0
+    accepted, out = accepted.view(B, L), out.view(B, L, D + 1)
+    best = accepted.argmax(1)
+    count = (accepted.gather(1, best[:, None])[:, 0] + 1).int()   # nodes to commit: the root and what agreed
+    path = branch[torch.arange(B, device=DEV), best].int().contiguous()
+    return path, count, out[torch.arange(B, device=DEV), best]
+
+
 def generate(seed=0, requests=3, rounds=20, beams=4, depth=3, page=16, drafts=True, keep=None, model=None):
     """Decodes `rounds` rounds greedily from one start token a request; `keep` bounds the caches by eviction.  Returns
     the requests' tokens and the caches' lengths."""
@@ -128,30 +154,12 @@ def generate(seed=0, requests=3, rounds=20, beams=4, depth=3, page=16, drafts=Tr
         cu = torch.arange(0, B * n + 1, n, dtype=torch.int32, device=DEV)
         logits, k_new, v_new, (q, lse) = model.run(tokens.flatten().long(), (place[:, None] + depths).flatten().long(),
                                                    cache, table, ctx, cu, n, masks.flatten()[:, None].contiguous())
-        # every branch from the root to a leaf, verified as a chain of drafts
-        leaves = torch.arange(leaf, n, device=DEV).expand(B, -1)
-        branch = [leaves]
-        for _ in range(int(depths[-1])):
-            branch.append(torch.gather(parents, 1, branch[-1]))
-        branch = torch.stack(branch[::-1], 2)                     # [B, leaves, depth + 1] nodes
-        L, D = branch.shape[1], branch.shape[2] - 1
-        rows = logits.view(B, n, -1)[torch.arange(B, device=DEV)[:, None, None], branch].flatten(0, 2).contiguous()
-        path_tokens = torch.gather(tokens, 1, branch.flatten(1)).view(B, L, D + 1).int()
-        cu_draft = torch.arange(0, B * L * D + 1, D, dtype=torch.int32, device=DEV) if D else torch.zeros(
-            B * L + 1, dtype=torch.int32, device=DEV)
-        proposed = path_tokens[:, :, 1:].reshape(-1).contiguous()     # held: this argument block keeps no tensor
-        out, accepted, status = sv.spec_verify_greedy(
-            sv.make_args(target=rows, cu_draft=cu_draft, draft_tokens=proposed, V=model.vocab, max_k=D))
-        assert int(status.abs().max()) == 0
-        accepted, out = accepted.view(B, L), out.view(B, L, D + 1)
-        best = accepted.argmax(1)
-        count = (accepted.gather(1, best[:, None])[:, 0] + 1).int()   # nodes to commit: the root and what agreed
-        path = branch[torch.arange(B, device=DEV), best].int().contiguous()
+        path, count, said = agree(model, logits, tokens, depths, parents, leaf)
+        D = path.shape[1] - 1
         new_len, status = sv.spec_cache_commit(
             sv.make_commit_args(k_new=k_new, v_new=v_new, cu_nodes=cu, path=path, path_len=count, cache=cache,
                                 block_table=table, ctx_len=ctx))
         assert int(status.abs().max()) == 0
-        said = out[torch.arange(B, device=DEV), best]
         for b, (m, toks) in enumerate(zip(count.tolist(), said.tolist())):
             text[b] += toks[:m]
         last = said.gather(1, count[:, None].long() - 1)[:, 0].contiguous()
