@@ -54,6 +54,32 @@ __device__ __forceinline__ float2 tmem_ld2(uint32_t addr) {
   return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
 
+// Scores of 16 lanes, 64 columns: of eight columns 8 g .., a thread has columns
+// 2 (lane % 4) and the one after of row lane / 4 (r[4 g], r[4 g + 1]) and of the
+// row 8 further (r[4 g + 2], r[4 g + 3]).
+__device__ __forceinline__ void tmem_ld_pairs(uint32_t addr, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+// And weights, two in a word: 32 columns, r[2 g] of the first row and r[2 g + 1]
+// of the second.
+__device__ __forceinline__ void tmem_st_pairs(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 struct C8Maps {
   CUtensorMap k, v;  // (channel, slot, head, page), bytes
 };
@@ -181,9 +207,10 @@ __device__ __forceinline__ float4 c8_scale(float ks, float vs) {
 //   thread, P = 2^(y - m) in fp16 over the scores read, O += P V (P from tensor
 //   memory), l += P / vs,
 // the products of one half running during the softmax of the other.
-template <typename T, int D, bool PAIR>
+template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kC8TcThreads, 1)
     cache8_tc_kernel(const Cache8Params C, const __grid_constant__ C8Maps maps, int box) {
+  constexpr bool PAIR = ROWS > kRows8, HALF = ROWS < kRows8;
   using S = C8Shape<D, PAIR>;
   const TreeParams& P = C.t;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -453,10 +480,12 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
         ok = ok && warp_wait(&h_full[v_slot], v_ph);
 #pragma unroll 1
         for (int h = 0; ok && h * kUnit8 < n16; ++h) {
-          ok = warp_wait(&p_ready[w * 2 + h], (p_ph >> h) & 1);
-          if (!ok) break;
-          p_ph ^= 1u << h;
-          tc_fence_after();
+          if (!HALF || h == 0) {
+            ok = warp_wait(&p_ready[w * 2 + h], (p_ph >> h) & 1);
+            if (!ok) break;
+            p_ph ^= 1u << h;
+            tc_fence_after();
+          }
           const uint64_t db = dv + (uint32_t)(v_slot * (S::kSlot >> 4) + h * (4 * 2048 >> 4));
           const uint32_t at = p + h * kUnit8, begun = h > 0 || i > first;
           const int steps = min(4, n16 / 16 - h * 4);
@@ -467,7 +496,7 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
 #pragma unroll 1
             for (int ks = 0; ks < steps; ++ks) mma_ts(o, at + ks * 8, db + ks * (2048 >> 4), id_v, ks > 0 || begun, one);
           }
-          if (h == 0) mma_commit(&o_half[w], one);
+          if (!HALF && h == 0) mma_commit(&o_half[w], one);
           if ((h + 1) * kUnit8 >= n16) {
             mma_commit(&o_done[w], one);  // before the scores that the softmax takes for a sign of it
             mma_commit(&h_empty[v_slot], one);
@@ -646,7 +675,8 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
     if (!ok) dead = 1;
   } else {
     // ----------------------------------------------------------- softmax
-    const int w = warp >> 2, row = (warp & 3) * 32 + lane, wtid = PAIR ? tid & 127 : tid;
+    const int w = warp >> 2, wtid = PAIR ? tid & 127 : tid;
+    const int row = HALF ? (warp & 3) * 16 + (lane & 15) : (warp & 3) * 32 + lane;
     const int tile = PAIR ? w : 0;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t o_at = tmem + lanes + 2 * kTcKeys + w * D;
@@ -657,6 +687,12 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
     uint32_t last_ph = 0;
     // node of a row: exact, as rows are at most 2^20 and half a row from a multiple
     const float inv_group = 1.f / (float)P.group;
+    // what two rows' threads know, for the row of a lane
+    auto of_row = [&](float a, float b) {
+      a = __shfl_sync(0xffffffffu, a, (lane & 7) * 4);
+      b = __shfl_sync(0xffffffffu, b, (lane & 7) * 4);
+      return lane & 8 ? b : a;
+    };
     bool ok = true;
     for (int seg = 0; ok; ++seg) {
       ok = wait_tile(tc);
@@ -672,9 +708,12 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
       constexpr int PER = D / 8, STEP = (PAIR ? 128 : 256) / PER;
       const int ch = wtid % PER;
       const T* src = static_cast<const T*>(P.q) + (long long)e.cu * P.sq_node + (long long)(e.kvh * P.group) * P.sq_head + ch * 8;
-      auto place = [&](int rr) { return qs + (ch >> 3) * (kRows8 * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4); };
+      auto place = [&](int rr) {
+        const int at = HALF ? rr + (rr & ~15) : rr;  // the lane of tensor memory
+        return qs + (ch >> 3) * (kRows8 * 128) + at * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+      };
 #pragma unroll 1
-      for (int rr = wtid / PER; rr < kRows8; rr += STEP) {
+      for (int rr = wtid / PER; rr < (HALF ? kRows8 / 2 : kRows8); rr += STEP) {
         const int R = row_lo + min(rr, max(nrows - 1, 0)), nd = (int)(((float)R + 0.5f) * inv_group);
         cp_async16(smem_u32(place(rr)), src + (long long)nd * P.sq_node + (long long)(R - nd * P.group) * P.sq_head, rr < nrows);
       }
@@ -701,11 +740,11 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
       mbar_arrive(&q_full[tile]);
       ok = warp_wait(&q_full[tile], seg & 1);  // the rows' scales
       if (!ok) break;
-      const bool mine = row < nrows;
-      const float rsc = !mine ? 0.f : kScaled<T> ? P.scale_log2 * __uint_as_float((uint32_t)(row_scale[tile][row] + 63) << 23) : P.scale_log2;
-      const bool any = (warp & 3) * 32 < nrows;  // warp-uniform
-      const int R = row_lo + (mine ? row : 0);
-      const int node = mine ? (int)(((float)R + 0.5f) * inv_group) : 0;
+      const bool here = row < nrows, mine = here && (!HALF || lane < 16);
+      const float rsc = !here ? 0.f : kScaled<T> ? P.scale_log2 * __uint_as_float((uint32_t)(row_scale[tile][row] + 63) << 23) : P.scale_log2;
+      const bool any = (warp & 3) * (HALF ? 16 : 32) < nrows;  // warp-uniform
+      const int R = row_lo + (here ? row : 0);
+      const int node = here ? (int)(((float)R + 0.5f) * inv_group) : 0;
       int seen = 0, see_lo = 0;  // as TreeRow
       if (e.part > 0 && any) {
         seen = c8_row(P, e.cu, e.n, node);
@@ -713,6 +752,10 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
       }
       float m = -INFINITY;                         // the row's reference, log2 units
       float2 l2 = make_float2(0.f, 0.f), l3 = l2;  // its sum
+      // of half a tile: of the thread's two rows
+      float m_b = -INFINITY;
+      const int src_a = lane >> 2, src_b = src_a + 8, pair = (lane & 3) * 2;  // their lanes, this thread's keys of eight
+      const float rsc_a = HALF ? __shfl_sync(0xffffffffu, rsc, src_a) : 0.f, rsc_b = HALF ? __shfl_sync(0xffffffffu, rsc, src_b) : 0.f;
       constexpr int TSTEP = PAIR ? 1 : 2;
       const int first = PAIR ? 0 : (tc ^ w) & 1;
       for (int i = first; ok && i < left; i += TSTEP, ++mine_tc) {
@@ -754,75 +797,87 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
           ok = warp_wait(&sc_full[at], ((tc + i) / kC8Tiles) & 1);
           if (!ok) break;
         }
-#pragma unroll 1
-        for (int h = 0; h * kUnit8 < n16; ++h) {
-          uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
-          if (masked && any) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int rest = valid - h * kUnit8 - c * 32;
-              bits[c] = rest >= 32 ? 0xffffffffu : (rest <= 0 ? 0u : (1u << rest) - 1u);
-              if (x.some()) bits[c] &= h == 0 ? see[c] : see[2 + c];
-            }
-          }
-          if (PAIR || h == 0) {
-            ok = ok && warp_wait(&s_full[w * 2 + h], (s_ph >> h) & 1);
-            s_ph ^= 1u << h;
-            if (!ok) break;
-            tc_fence_after();
-          }
-          const uint32_t s_at = tmem + lanes + w * kTcKeys + h * kUnit8;
+        if constexpr (HALF) {
+          ok = warp_wait(&s_full[w * 2], s_ph);
+          s_ph ^= 1u;
+          if (!ok) break;
+          tc_fence_after();
           if (any) {
-            float z[kUnit8];
-            tmem_ld32(s_at, z);
-            tmem_ld32(s_at + 32, z + 32);
-            const float4* sc = &scales[at][h * 4];
+            const uint32_t s_at = tmem + lanes + w * kTcKeys;
+            float z[kTcKeys / 2];  // of eight keys: two of row a, two of row b
+            tmem_ld_pairs(s_at, z);
+            tmem_ld_pairs(s_at + 64, z + 32);
+            const float4* sc = scales[at];
             tmem_wait_ld();
             loaded(z);
             loaded(z + 32);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < kTcKeys / 16; ++q) {
               const float4 e4 = sc[q];
-              const float2 c2 = make_float2(e4.x * rsc, e4.x * rsc), b2 = make_float2(e4.y, e4.y);
+              const float2 ca = make_float2(e4.x * rsc_a, e4.x * rsc_a), cb = make_float2(e4.x * rsc_b, e4.x * rsc_b);
+              const float2 b2 = make_float2(e4.y, e4.y);
 #pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                const float2 y = __ffma2_rn(make_float2(z[q * 16 + k], z[q * 16 + k + 1]), c2, b2);
-                z[q * 16 + k] = y.x;
-                z[q * 16 + k + 1] = y.y;
+              for (int k = q * 8; k < q * 8 + 8; k += 4) {
+                const float2 a = __ffma2_rn(make_float2(z[k], z[k + 1]), ca, b2), b = __ffma2_rn(make_float2(z[k + 2], z[k + 3]), cb, b2);
+                z[k] = a.x;
+                z[k + 1] = a.y;
+                z[k + 2] = b.x;
+                z[k + 3] = b.y;
               }
             }
             if (masked) {  // -inf where the row sees nothing
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
+              for (int c = 0; c < 4; ++c) {
+                const int rest = valid - c * 32;
+                uint32_t bits = rest >= 32 ? 0xffffffffu : (rest <= 0 ? 0u : (1u << rest) - 1u);
+                if (x.some()) bits &= see[c];
+                const uint32_t ba = __shfl_sync(0xffffffffu, bits, src_a) >> pair, bb = __shfl_sync(0xffffffffu, bits, src_b) >> pair;
 #pragma unroll
-                for (int k = 0; k < 32; ++k) z[c * 32 + k] = (bits[c] >> k) & 1u ? z[c * 32 + k] : -INFINITY;
-            }
-            float top[4];
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) top[k] = fmaxf(z[2 * k], z[2 * k + 1]);
-#pragma unroll
-            for (int q = 8; q < kUnit8; q += 8)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], z[q + 2 * k]), z[q + 2 * k + 1]);
-            const float zx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            const bool move = zx > m + kLazy8 || (m == -INFINITY && zx > -INFINITY);
-            if (__any_sync(0xffffffffu, move)) {
-              const float f = move ? (m == -INFINITY ? 0.f : ex2(m - zx)) : 1.f;
-              if (move) {
-                m = zx;
-                l2.x *= f;
-                l2.y *= f;
-                l3.x *= f;
-                l3.y *= f;
+                  for (int j = 0; j < 2; ++j) {
+                    float* y = z + c * 16 + k * 4 + j;
+                    y[0] = (ba >> (k * 8 + j)) & 1u ? y[0] : -INFINITY;
+                    y[2] = (bb >> (k * 8 + j)) & 1u ? y[2] : -INFINITY;
+                  }
               }
-              if (i > first || h > 0) {
-                // The unit before is in O.  Each barrier is at most one phase
-                // behind, as the scores here came after the products before.
-                if (mine_tc > 0) ok = warp_wait(&o_done[w], (mine_tc - 1) & 1);
-                if (h > 0) ok = ok && warp_wait(&o_half[w], mine_tc & 1);
+            }
+            float ta[2], tb[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              ta[k] = fmaxf(z[4 * k], z[4 * k + 1]);
+              tb[k] = fmaxf(z[4 * k + 2], z[4 * k + 3]);
+            }
+#pragma unroll
+            for (int q = 8; q < kTcKeys / 2; q += 8)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                ta[k] = fmaxf(fmaxf(ta[k], z[q + 4 * k]), z[q + 4 * k + 1]);
+                tb[k] = fmaxf(fmaxf(tb[k], z[q + 4 * k + 2]), z[q + 4 * k + 3]);
+              }
+            float za = fmaxf(ta[0], ta[1]), zb = fmaxf(tb[0], tb[1]);
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+              za = fmaxf(za, __shfl_xor_sync(0xffffffffu, za, o));
+              zb = fmaxf(zb, __shfl_xor_sync(0xffffffffu, zb, o));
+            }
+            const bool move_a = za > m + kLazy8 || (m == -INFINITY && za > -INFINITY);
+            const bool move_b = zb > m_b + kLazy8 || (m_b == -INFINITY && zb > -INFINITY);
+            if (__any_sync(0xffffffffu, move_a || move_b)) {
+              const float fa = move_a ? (m == -INFINITY ? 0.f : ex2(m - za)) : 1.f;
+              const float fb = move_b ? (m_b == -INFINITY ? 0.f : ex2(m_b - zb)) : 1.f;
+              m = move_a ? za : m;
+              m_b = move_b ? zb : m_b;
+              l2.x *= fa;
+              l2.y *= fa;
+              l3.x *= fb;
+              l3.y *= fb;
+              if (i > first) {
+                ok = warp_wait(&o_done[w], (mine_tc - 1) & 1);
                 if (!ok) break;
                 __syncwarp();
                 tc_fence_after();
+                const float f = of_row(fa, fb);
 #pragma unroll 1
                 for (int c = 0; c < D / 16; ++c) {
                   uint32_t o[16];
@@ -833,31 +888,137 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
                 }
               }
             }
-            const float ref = m == -INFINITY ? 0.f : m - kTop8;
-            const float2 nr = make_float2(-ref, -ref);
+            const float ref_a = m == -INFINITY ? 0.f : m - kTop8, ref_b = m_b == -INFINITY ? 0.f : m_b - kTop8;
+            const float2 na = make_float2(-ref_a, -ref_a), nb = make_float2(-ref_b, -ref_b);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               uint32_t p[16];
 #pragma unroll
-              for (int k = 0; k < 32; k += 4) {
-                const float iv = sc[c * 2 + k / 16].z;
+              for (int k = 0; k < 8; ++k) {
+                const float iv = sc[c * 4 + k / 2].z;
                 const float2 i2 = make_float2(iv, iv);
-                const float* y = z + c * 32 + k;
-                const float2 a = __fadd2_rn(make_float2(y[0], y[1]), nr);
-                const float2 b = __fadd2_rn(make_float2(y[2], y[3]), nr);
+                const float* y = z + c * 32 + k * 4;
+                const float2 a = __fadd2_rn(make_float2(y[0], y[1]), na);
+                const float2 b = __fadd2_rn(make_float2(y[2], y[3]), nb);
                 const float2 ea = make_float2(ex2(a.x), ex2(a.y)), eb = make_float2(ex2(b.x), ex2(b.y));
                 l2 = __ffma2_rn(ea, i2, l2);
                 l3 = __ffma2_rn(eb, i2, l3);
-                p[k / 2] = pack2<__half>(ea.x, ea.y);
-                p[k / 2 + 1] = pack2<__half>(eb.x, eb.y);
+                p[2 * k] = pack2<__half>(ea.x, ea.y);
+                p[2 * k + 1] = pack2<__half>(eb.x, eb.y);
               }
-              tmem_st16(s_at + c * 16, p);
+              tmem_st_pairs(s_at + c * kUnit8, p);
             }
             tc_wait_st();
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_ready[w * 2 + h]);
+          if (lane == 0) mbar_arrive(&p_ready[w * 2]);
+        } else {
+#pragma unroll 1
+          for (int h = 0; h * kUnit8 < n16; ++h) {
+            uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
+            if (masked && any) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int rest = valid - h * kUnit8 - c * 32;
+                bits[c] = rest >= 32 ? 0xffffffffu : (rest <= 0 ? 0u : (1u << rest) - 1u);
+                if (x.some()) bits[c] &= h == 0 ? see[c] : see[2 + c];
+              }
+            }
+            if (PAIR || h == 0) {
+              ok = ok && warp_wait(&s_full[w * 2 + h], (s_ph >> h) & 1);
+              s_ph ^= 1u << h;
+              if (!ok) break;
+              tc_fence_after();
+            }
+            const uint32_t s_at = tmem + lanes + w * kTcKeys + h * kUnit8;
+            if (any) {
+              float z[kUnit8];
+              tmem_ld32(s_at, z);
+              tmem_ld32(s_at + 32, z + 32);
+              const float4* sc = &scales[at][h * 4];
+              tmem_wait_ld();
+              loaded(z);
+              loaded(z + 32);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float4 e4 = sc[q];
+                const float2 c2 = make_float2(e4.x * rsc, e4.x * rsc), b2 = make_float2(e4.y, e4.y);
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                  const float2 y = __ffma2_rn(make_float2(z[q * 16 + k], z[q * 16 + k + 1]), c2, b2);
+                  z[q * 16 + k] = y.x;
+                  z[q * 16 + k + 1] = y.y;
+                }
+              }
+              if (masked) {  // -inf where the row sees nothing
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) z[c * 32 + k] = (bits[c] >> k) & 1u ? z[c * 32 + k] : -INFINITY;
+              }
+              float top[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) top[k] = fmaxf(z[2 * k], z[2 * k + 1]);
+#pragma unroll
+              for (int q = 8; q < kUnit8; q += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], z[q + 2 * k]), z[q + 2 * k + 1]);
+              const float zx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+              const bool move = zx > m + kLazy8 || (m == -INFINITY && zx > -INFINITY);
+              if (__any_sync(0xffffffffu, move)) {
+                const float f = move ? (m == -INFINITY ? 0.f : ex2(m - zx)) : 1.f;
+                if (move) {
+                  m = zx;
+                  l2.x *= f;
+                  l2.y *= f;
+                  l3.x *= f;
+                  l3.y *= f;
+                }
+                if (i > first || h > 0) {
+                  // The unit before is in O.  Each barrier is at most one phase
+                  // behind, as the scores here came after the products before.
+                  if (mine_tc > 0) ok = warp_wait(&o_done[w], (mine_tc - 1) & 1);
+                  if (h > 0) ok = ok && warp_wait(&o_half[w], mine_tc & 1);
+                  if (!ok) break;
+                  __syncwarp();
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int c = 0; c < D / 16; ++c) {
+                    uint32_t o[16];
+                    tmem_ld16(o_at + c * 16, o);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st16(o_at + c * 16, o);
+                  }
+                }
+              }
+              const float ref = m == -INFINITY ? 0.f : m - kTop8;
+              const float2 nr = make_float2(-ref, -ref);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint32_t p[16];
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                  const float iv = sc[c * 2 + k / 16].z;
+                  const float2 i2 = make_float2(iv, iv);
+                  const float* y = z + c * 32 + k;
+                  const float2 a = __fadd2_rn(make_float2(y[0], y[1]), nr);
+                  const float2 b = __fadd2_rn(make_float2(y[2], y[3]), nr);
+                  const float2 ea = make_float2(ex2(a.x), ex2(a.y)), eb = make_float2(ex2(b.x), ex2(b.y));
+                  l2 = __ffma2_rn(ea, i2, l2);
+                  l3 = __ffma2_rn(eb, i2, l3);
+                  p[k / 2] = pack2<__half>(ea.x, ea.y);
+                  p[k / 2 + 1] = pack2<__half>(eb.x, eb.y);
+                }
+                tmem_st16(s_at + c * 16, p);
+              }
+              tc_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_ready[w * 2 + h]);
+          }
         }
       }
       if (!ok) break;
@@ -870,6 +1031,16 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
         if (!ok) break;
       }
       float l = (l2.x + l2.y) + (l3.x + l3.y);
+      if (HALF) {
+        float la = l2.x + l2.y, lb = l3.x + l3.y;
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          la += __shfl_xor_sync(0xffffffffu, la, o);
+          lb += __shfl_xor_sync(0xffffffffu, lb, o);
+        }
+        l = of_row(la, lb);
+        m = of_row(m, m_b);
+      }
       if (!PAIR && any) tmem_st2(tmem + lanes + w * kTcKeys, m, l);  // where the scores were
       tc_fence_before();
       // both streams are done: with the queries, and with each other's outputs
@@ -971,22 +1142,29 @@ bool encode8(CUtensorMap* m, const TreeParams& P, const void* base, int box) {
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, bool PAIR>
+template <typename T, int D, int ROWS>
 int launch_c8(const Cache8Params& C, const C8Maps& maps, int box, cudaStream_t s) {
-  using S = C8Shape<D, PAIR>;
-  if (cudaFuncSetAttribute(cache8_tc_kernel<T, D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) !=
+  using S = C8Shape<D, (ROWS > kRows8)>;
+  if (cudaFuncSetAttribute(cache8_tc_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) !=
       cudaSuccess) {
     cudaGetLastError();
     return -1;
   }
-  return launch_kernel(cache8_tc_kernel<T, D, PAIR>, dim3(C.t.grid), kC8TcThreads, S::kSmem, s, C, maps, box);
+  return launch_kernel(cache8_tc_kernel<T, D, ROWS>, dim3(C.t.grid), kC8TcThreads, S::kSmem, s, C, maps, box);
+}
+
+template <typename T, int D>
+int launch_c8_shape(const Cache8Params& C, const C8Maps& maps, int box, cudaStream_t s) {
+  switch (C.t.rows) {
+    case kRows8 / 2: return launch_c8<T, D, kRows8 / 2>(C, maps, box, s);
+    case kRows8: return launch_c8<T, D, kRows8>(C, maps, box, s);
+    default: return launch_c8<T, D, 2 * kRows8>(C, maps, box, s);
+  }
 }
 
 template <typename T>
-int launch_c8_shape(const Cache8Params& C, const C8Maps& maps, int box, cudaStream_t s) {
-  const bool pair = C.t.rows > kRows8;
-  if (C.t.dim == 64) return pair ? launch_c8<T, 64, true>(C, maps, box, s) : launch_c8<T, 64, false>(C, maps, box, s);
-  return pair ? launch_c8<T, 128, true>(C, maps, box, s) : launch_c8<T, 128, false>(C, maps, box, s);
+int launch_c8_dim(const Cache8Params& C, const C8Maps& maps, int box, cudaStream_t s) {
+  return C.t.dim == 64 ? launch_c8_shape<T, 64>(C, maps, box, s) : launch_c8_shape<T, 128>(C, maps, box, s);
 }
 
 }  // namespace
@@ -1002,7 +1180,7 @@ TreePlan plan_cache8_tc(int rows, int num_sms) {
   TreePlan p;
   p.kernel = 1;
   p.grid = num_sms;
-  p.rows = rows > kRows8 ? 2 * kRows8 : kRows8;
+  p.rows = rows > kRows8 ? 2 * kRows8 : rows > kRows8 / 2 ? kRows8 : kRows8 / 2;
   p.kt = kTcKeys;
   return p;
 }
@@ -1011,7 +1189,7 @@ int launch_cache8_tc(const Cache8Params& C, bool bf16, cudaStream_t s) {
   C8Maps maps;
   const int box = page_box(C.t.page_size);
   if (!encode8(&maps.k, C.t, C.t.k, box) || !encode8(&maps.v, C.t, C.t.v, box)) return -1;
-  return bf16 ? launch_c8_shape<__nv_bfloat16>(C, maps, box, s) : launch_c8_shape<__half>(C, maps, box, s);
+  return bf16 ? launch_c8_dim<__nv_bfloat16>(C, maps, box, s) : launch_c8_dim<__half>(C, maps, box, s);
 }
 
 }  // namespace sv

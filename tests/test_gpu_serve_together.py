@@ -258,6 +258,17 @@ def test_attention_past_32_bit_offsets():
     assert torch.equal(small.run()[0], want)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("window", [None, 130])
+@pytest.mark.parametrize("dim,group,nodes", [(128, 1, (17, 31)), (128, 2, (32, 9)), (64, 1, (33, 64)), (128, 1, (65, 3)),
+                                             (64, 2, (64, 33)), (128, 1, (129, 64)), (128, 7, (9, 3))])
+def test_numbers_of_rows_over_8_bits(dim, group, nodes, window, dtype):
+    """Up to 64 rows a key head, up to 128, and more, of a few tiles and of many that several CTAs share."""
+    for ctx in ([130, 257], [6000, 1]):
+        Case(dtype=dtype, dim=dim, kv=2, group=group, page=16, ctx=ctx, nodes=list(nodes), chain=False, window=window,
+             sinks=3 if window else 0, block=16, seed=sum(nodes) + group).check()
+
+
 @pytest.mark.parametrize("beams,depth", [(4, 3), (1, 5), (10, 2)])
 def test_the_example_of_long_texts(beams, depth):
     import long_text as E
