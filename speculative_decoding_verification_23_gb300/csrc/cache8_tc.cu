@@ -501,11 +501,15 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
             mma_commit(&o_done[w], one);  // before the scores that the softmax takes for a sign of it
             mma_commit(&h_empty[v_slot], one);
           }
-          if (PAIR && next > h * kUnit8) scores(next, h);
+          if (PAIR && next > h * kUnit8 && (next > kUnit8 || n16 <= kUnit8)) scores(next, h);
         }
         if (!ok) break;
-        // what the tile had no half for
-        if (PAIR ? n16 <= kUnit8 && next > kUnit8 : next > 0) scores(next, PAIR ? 1 : 0);
+        // What the tile had no half for, and the scores of half a tile after a whole
+        // one.  Three slots take keys and values in turn, and the conversion of values
+        // relies on this order: the slot of a tile's keys is not free before that of
+        // the values of the tile before, or a phase of the latter's could be mistaken
+        // for the one two further.
+        if (PAIR ? (n16 <= kUnit8) == (next > kUnit8) && next > 0 : next > 0) scores(next, PAIR && next > kUnit8 ? 1 : 0);
         v_slot += 2 * STEP;
         if (v_slot >= S::kSlots) {
           v_slot -= S::kSlots;
