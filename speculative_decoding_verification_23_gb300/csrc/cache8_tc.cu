@@ -517,7 +517,11 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
         }
         if (i + STEP >= left) mma_commit(&o_last[w], one);
         leave_tile(tc + i);
-        if (!PAIR && i + 1 < left) leave_tile(tc + i + 1);
+        if (!PAIR && i + 1 < left) {  // the other stream's; not before it is described, or it would count for the one before
+          ok = wait_tile(tc + i + 1);
+          if (!ok) break;
+          leave_tile(tc + i + 1);
+        }
         n16 = next;
         next = i + 2 * STEP < left ? tile_keys(tc + i + 2 * STEP) : 0;
       }
