@@ -308,31 +308,39 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
       x.count = 0;
       x.d.info = x.d.pos = 0;
       x.e.bad = 0;
+      // this lane's tile is tile t of the segment
+      auto fill = [&](int t) {
+        const C8Tile y = c8_tile(walk.r, t);
+        x.d.lo = y.lo;
+        x.d.info = y.valid | (y.cached ? kTileCached : 0) | (y.some ? kTileSome : 0);
+        x.d.pos = t - g.t0;
+        x.d.left = g.t1 - t;
+        x.e.b = g.b;
+        x.e.kvh = g.kvh;
+        x.e.m = g.m;
+        x.e.cu = walk.r.cu;
+        x.e.n = walk.r.n;
+        x.e.ctx = walk.r.ctx;
+        x.e.part = walk.r.part;
+        x.e.t0 = g.t0;
+        x.e.t1 = g.t1;
+        x.e.whole = g.t0 == 0 && g.t1 == walk.r.per_item;
+      };
+      if (t + 4 <= g.t1) {  // most often
+        fill(t + sub);
+        t += 4;
+        x.count = 4;
+      } else {
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        if (t >= g.t1) {
-          if (!walk.next(P, g)) break;
-          t = g.t0;
+        for (int i = 0; i < 4; ++i) {
+          if (t >= g.t1) {
+            if (!walk.next(P, g)) break;
+            t = g.t0;
+          }
+          if (sub == i) fill(t);
+          ++t;
+          ++x.count;
         }
-        if (sub == i) {
-          const C8Tile y = c8_tile(walk.r, t);
-          x.d.lo = y.lo;
-          x.d.info = y.valid | (y.cached ? kTileCached : 0) | (y.some ? kTileSome : 0);
-          x.d.pos = t - g.t0;
-          x.d.left = g.t1 - t;
-          x.e.b = g.b;
-          x.e.kvh = g.kvh;
-          x.e.m = g.m;
-          x.e.cu = walk.r.cu;
-          x.e.n = walk.r.n;
-          x.e.ctx = walk.r.ctx;
-          x.e.part = walk.r.part;
-          x.e.t0 = g.t0;
-          x.e.t1 = g.t1;
-          x.e.whole = g.t0 == 0 && g.t1 == walk.r.per_item;
-        }
-        ++t;
-        ++x.count;
       }
       x.page = x.slot = 0;
       x.ks = x.vs = 0.f;

@@ -258,6 +258,18 @@ def test_attention_past_32_bit_offsets():
     assert torch.equal(small.run()[0], want)
 
 
+@pytest.mark.parametrize("dim,group,nodes", [(128, 4, 64), (64, 8, 40), (128, 2, 30), (128, 2, 60), (64, 2, 50), (64, 1, 17)])
+def test_many_tiles_give_the_same_bits_again(dim, group, nodes):
+    """Dozens of tiles of every CTA, in segments of all lengths, many times."""
+    rng, kv, page, B = np.random.RandomState(3), 8, 16, 12
+    c = Case(dtype="fp16", dim=dim, kv=kv, group=group, page=page, ctx=rng.randint(1000, 9000, B).tolist(), nodes=[nodes] * B,
+             chain=False, block=16, seed=4)
+    args = c.args()
+    want = c.run(args)
+    for _ in range(60):
+        assert all(torch.equal(x, y) for x, y in zip(c.run(args), want))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("window", [None, 130])
 @pytest.mark.parametrize("dim,group,nodes", [(128, 1, (17, 31)), (128, 2, (32, 9)), (64, 1, (33, 64)), (128, 1, (65, 3)),
