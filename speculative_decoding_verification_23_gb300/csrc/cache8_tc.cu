@@ -439,7 +439,8 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
     uint32_t k_ph = 0, v_ph = 0;
     const uint64_t da = smem_desc(smem_u32(smem) + (PAIR ? w : 0) * S::kQBytes, 16, 1024);
     const uint64_t dk = smem_desc(smem_u32(ring), 16, 1024), dv = smem_desc(smem_u32(ring), S::kHalf, 1024);
-    const uint32_t o = tmem + 2 * kTcKeys + w * D, id_v = inst_desc<__half>(D, true), p = tmem + w * kTcKeys;
+    constexpr uint32_t kFewer = HALF ? 4u << 24 : 0u;  // 64 rows: 16 lanes of each warp's 32
+    const uint32_t o = tmem + 2 * kTcKeys + w * D, id_v = inst_desc<__half>(D, true) - kFewer, p = tmem + w * kTcKeys;
     auto tile_keys = [&](int i) {  // of tile i, by sixteens
       ok = ok && wait_tile(i);
       return ok ? uniform(tiles[i & (kC8Tiles - 1)].n16()) : 0;
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
     // Scores: with two row tiles of a half as soon as the weights there have been
     // used; with two streams of 128 keys at once, which reads the queries once.
     auto scores = [&](int n16, int h) {
-      const uint32_t id = inst_desc<__half>(PAIR ? min(kUnit8, n16 - h * kUnit8) : n16, false);
+      const uint32_t id = inst_desc<__half>(PAIR ? min(kUnit8, n16 - h * kUnit8) : n16, false) - kFewer;
       const uint64_t db = dk + (uint32_t)(k_slot * (S::kSlot >> 4) + h * ((kUnit8 * 128) >> 4));
       if (h == 0) ok = ok && warp_wait(&h_full[k_slot], k_ph);
       if (!ok) return;
@@ -725,8 +726,7 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
       const int ch = wtid % PER;
       const T* src = static_cast<const T*>(P.q) + (long long)e.cu * P.sq_node + (long long)(e.kvh * P.group) * P.sq_head + ch * 8;
       auto place = [&](int rr) {
-        const int at = HALF ? rr + (rr & ~15) : rr;  // the lane of tensor memory
-        return qs + (ch >> 3) * (kRows8 * 128) + at * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+        return qs + (ch >> 3) * (kRows8 * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
       };
 #pragma unroll 1
       for (int rr = wtid / PER; rr < (HALF ? kRows8 / 2 : kRows8); rr += STEP) {
