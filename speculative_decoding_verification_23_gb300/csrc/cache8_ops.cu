@@ -21,43 +21,46 @@ __device__ __forceinline__ float scale_for(float top) {
 // x * inv, infinities as NaN (the conversion would saturate them).
 __device__ __forceinline__ float to8_arg(float x, float inv) { return fmaf(x, 0.f, x * inv); }
 
-// The request's tokens and pages, found sound or not: every thread of a CTA
-// comes here.
+// A request's path: its first row and nodes, tokens to write, and the length
+// before them.
 struct Path8 {
-  int cu, m, ctx, status;
+  int cu, n, m, ctx;
 };
-__device__ __forceinline__ Path8 check_path(const Commit8Params& P, int b) {
+__device__ __forceinline__ Path8 read_path(const Commit8Params& P, int b) {
   Path8 r;
   r.cu = P.cu[b];
-  const int n = P.cu[b + 1] - r.cu;
+  r.n = P.cu[b + 1] - r.cu;
   r.m = P.path_len[b];
   r.ctx = P.ctx[b];
-  const bool ok = r.cu >= 0 && n >= 0 && (long long)r.cu + n <= P.total && r.m >= 0 && r.m <= P.ld_path && r.ctx >= 0 &&
-                  (long long)r.ctx + r.m <= (long long)P.ld_table * P.page_size;
-  const PageDiv pd(P.page_size);
-  int bad = 0;
-  if (ok) {
-    const int32_t* path = P.path + (long long)b * P.ld_path;
-    for (int i = threadIdx.x; i < r.m; i += kC8Threads) {
-      const int node = path[i];
-      bad |= node < 0 || node >= n ? 1 : 0;
-    }
-    if (r.m > 0) {
-      int first, last, slot;
-      pd.split(r.ctx, first, slot);
-      pd.split(r.ctx + r.m - 1, last, slot);
-      for (int p = first + (int)threadIdx.x; p <= last; p += kC8Threads) {
-        const int id = P.table[(long long)b * P.ld_table + p];
-        bad |= id < 0 || id >= P.num_pages ? 2 : 0;
-      }
-    }
-  }
-  r.status = ok ? 0 : kStatusBadLen;
-  if (__syncthreads_or(bad)) {
-    if (__syncthreads_or(bad & 1)) r.status |= kStatusBadLen;
-    if (__syncthreads_or(bad & 2)) r.status |= kStatusBadPage;
-  }
   return r;
+}
+__device__ __forceinline__ bool lengths_ok(const Commit8Params& P, const Path8& r) {
+  return r.cu >= 0 && r.n >= 0 && (long long)r.cu + r.n <= P.total && r.m >= 0 && r.m <= P.ld_path && r.ctx >= 0 &&
+         (long long)r.ctx + r.m <= (long long)P.ld_table * P.page_size;
+}
+// Bit 0: a node outside the tree, bit 1: a bad page; thread `tid` of `threads`
+// looks at every threads-th.
+__device__ __forceinline__ int look_path(const Commit8Params& P, const Path8& r, int b, int tid, int threads) {
+  int bad = 0;
+  const int32_t* path = P.path + (long long)b * P.ld_path;
+  for (int i = tid; i < r.m; i += threads) {
+    const int node = path[i];
+    bad |= node < 0 || node >= r.n ? 1 : 0;
+  }
+  if (r.m > 0) {
+    const PageDiv pd(P.page_size);
+    int first, last, slot;
+    pd.split(r.ctx, first, slot);
+    pd.split(r.ctx + r.m - 1, last, slot);
+    for (int p = first + tid; p <= last; p += threads) {
+      const int id = P.table[(long long)b * P.ld_table + p];
+      bad |= id < 0 || id >= P.num_pages ? 2 : 0;
+    }
+  }
+  return bad;
+}
+__device__ __forceinline__ int path_status(bool ok, int bad) {
+  return (ok && !(bad & 1) ? 0 : kStatusBadLen) | (bad & 2 ? kStatusBadPage : 0);
 }
 
 // A barrier of the warps that share a unit (constant ids: a barrier that is not
@@ -75,10 +78,14 @@ __device__ __forceinline__ void unit_sync(int group, int threads) {
 __global__ void __launch_bounds__(kC8Threads) commit8_check_kernel(const Commit8Params P) {
   after_previous();
   const int b = blockIdx.x;
-  const Path8 r = check_path(P, b);
+  const Path8 r = read_path(P, b);
+  const bool ok = lengths_ok(P, r);
+  int bad = ok ? look_path(P, r, b, threadIdx.x, kC8Threads) : 0;
+  if (__syncthreads_or(bad)) bad = (__syncthreads_or(bad & 1) ? 1 : 0) | (__syncthreads_or(bad & 2) ? 2 : 0);
   if (threadIdx.x == 0) {
-    if (P.status) P.status[b] = r.status;
-    P.new_len[b] = r.status ? -1 : r.ctx + r.m;
+    const int status = path_status(ok, bad);
+    if (P.status) P.status[b] = status;
+    P.new_len[b] = status ? -1 : r.ctx + r.m;
   }
 }
 
@@ -107,11 +114,13 @@ __device__ __forceinline__ uint32_t max_size2<__nv_bfloat16>(uint32_t a, uint32_
 // (registers for them would leave too few warps).  A warp with more than 16 rows
 // of a unit goes over them twice, for the size and for the bytes.
 //
-// The CTAs of a request share its units evenly, over all layers, so that each
-// looks at the request's lengths and path once for many of them.
+// The groups of warps share the units of all requests evenly, each a run of them
+// (over a request's layers, blocks and heads), so that each looks at a request's
+// lengths and path once for many.
 //
 // CHECKED: the check kernel has run, and a new length of -1 says that the
-// request is bad.  Otherwise every CTA checks its request.
+// request is bad.  Otherwise every group checks the requests of its units, and
+// the one with a request's first unit tells the caller.
 template <int D>
 struct C8Stage {
   static constexpr int kBytes = kC8Rows * D * 2;               // of a warp's step
@@ -138,65 +147,120 @@ __global__ void __launch_bounds__(kC8Threads, D <= 128 ? 2 : 1) commit8_kernel(c
   __shared__ float tops[2][kC8Warps];
   __shared__ C8Unit info[kC8Warps][S::kStages];
   after_previous();
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const PageDiv pd(P.page_size), bd(P.block);
+  const int W = P.warps, group = warp / W, wsub = warp % W, groups = kC8Warps / W;
+  // Requests: their units, and a lane's sum of those of its requests.
   Path8 r;
-  if (CHECKED) {
-    r.cu = P.cu[b];
-    r.m = P.path_len[b];
-    const int len = P.new_len[b];
-    r.status = len < 0;
-    r.ctx = len - r.m;
-  } else {
-    r = check_path(P, b);
-    if (blockIdx.y == 0 && tid == 0) {
-      if (P.status) P.status[b] = r.status;
-      P.new_len[b] = r.status ? -1 : r.ctx + r.m;
+  int first_block = 0, of_layer = 0;  // heads change first: neighbours' rows lie side by side
+  auto request = [&](int b) {         // returns the units
+    if (CHECKED) {
+      r.cu = P.cu[b];
+      r.m = P.path_len[b];
+      const int len = P.new_len[b];
+      r.ctx = len - r.m;
+      if (len < 0) r.m = 0;
+    } else {
+      r = read_path(P, b);
+      if (!lengths_ok(P, r)) r.m = -1;
+    }
+    if (r.m <= 0) return 0ll;
+    int last_block, rest;
+    bd.split(r.ctx, first_block, rest);
+    bd.split(r.ctx + r.m - 1, last_block, rest);
+    of_layer = (last_block - first_block + 1) * P.heads * 2;
+    return (long long)of_layer * P.layers;
+  };
+  const int per_lane = (P.B + 31) / 32;
+  long long mine = 0;
+  for (int b = lane * per_lane; b < min(P.B, (lane + 1) * per_lane); ++b) {
+    const long long units = request(b);
+    mine += units;
+    if (!CHECKED && units == 0 && blockIdx.x == 0 && warp == 0) {  // nothing to write, or bad
+      const int status = path_status(r.m == 0, 0);
+      if (P.status) P.status[b] = status;
+      P.new_len[b] = status ? -1 : r.ctx;
     }
   }
-  if (r.status || r.m == 0) return;
-  const PageDiv pd(P.page_size), bd(P.block);
-  const int32_t* path = P.path + (long long)b * P.ld_path;
-  const int32_t* table = P.table + (long long)b * P.ld_table;
-  const int W = P.warps, group = warp / W, wsub = warp % W, groups = kC8Warps / W;
-  int first_block, last_block, rest;
-  bd.split(r.ctx, first_block, rest);
-  bd.split(r.ctx + r.m - 1, last_block, rest);
-  const int of_layer = (last_block - first_block + 1) * P.heads * 2;  // heads change first: neighbours' rows lie side by side
-  const long long units = (long long)of_layer * P.layers;
+  long long before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  const long long total = __shfl_sync(0xffffffffu, before, 31), all = (long long)gridDim.x * groups;
+  before -= mine;
+  const long long at_group = (long long)blockIdx.x * groups + group;
+  const long long u_from = div_fast(at_group * total, all), u_to = div_fast((at_group + 1) * total, all);
+  if (u_from == u_to) return;  // every warp of the group
+  // The request of the first unit.
+  int b = 0;
+  long long first = before;
+  {
+    const bool me = u_from >= before && u_from < before + mine;
+    if (me)
+      for (b = lane * per_lane;; ++b) {
+        const long long units = request(b);
+        if (u_from < first + units) break;
+        first += units;
+      }
+    const int src = __ffs(__ballot_sync(0xffffffffu, me)) - 1;
+    b = __shfl_sync(0xffffffffu, b, src);
+    first = __shfl_sync(0xffffffffu, first, src);
+  }
+  long long units = request(b);
+  const int32_t* path = nullptr;
+  const int32_t* table = nullptr;
+  bool sound = true;
+  auto begin = [&](long long u) {  // a request, whose unit u is the group's first
+    path = P.path + (long long)b * P.ld_path;
+    table = P.table + (long long)b * P.ld_table;
+    if (!CHECKED) {
+      const int bad = __reduce_or_sync(0xffffffffu, look_path(P, r, b, lane, 32));
+      sound = bad == 0;
+      if (u == first && wsub == 0 && lane == 0) {
+        if (P.status) P.status[b] = path_status(true, bad);
+        P.new_len[b] = bad ? -1 : r.ctx + r.m;
+      }
+    }
+  };
+  begin(u_from);
   const int per = (P.block + W - 1) / W;        // rows of a warp
   const int w_rows = max(0, min(per, P.block - wsub * per));
   const int passes = (per + kC8Rows - 1) / kC8Rows, steps = passes == 1 ? 1 : 2 * passes;  // of a unit
   const int rsub = lane / LR, ch = (lane % LR) * 8;
   const bool lane_on = rsub < R;
-  // every warp of a CTA takes the same number of turns
-  const long long stride = (long long)gridDim.y * groups, u_base = (long long)blockIdx.y * groups;
   unsigned char* stage = smem + warp * (S::kStages * S::kBytes);
   const uint32_t stage_at = smem_u32(stage) + lane * 16;
   // The copies: of unit after unit, step after step.
-  long long base_ahead = u_base;
+  long long u_ahead = u_from;
   int step_ahead = 0, slot_ahead = 0, q0 = 0, q1 = 0, w0 = 0;
   const T* x = nullptr;
   auto copy = [&]() {
-    if (base_ahead < units) {
+    if (u_ahead < u_to) {
       if (step_ahead == 0) {  // the next unit
-        const bool mine = base_ahead + group < units;
-        const long long u = mine ? base_ahead + group : 0;
+        while (u_ahead >= first + units) {  // ends: some request holds unit u_ahead < total
+          first += units;
+          units = request(++b);
+          if (units > 0) begin(u_ahead);
+        }
+        const long long u = u_ahead - first;
         const int layer = (int)div_fast(u, of_layer), o = (int)(u - (long long)layer * of_layer), kv = o & 1;
         const int j = (int)((uint32_t)(o >> 1) / (uint32_t)P.heads), h = (o >> 1) - j * P.heads;
         const int base = (first_block + j) * P.block;
         w0 = base + wsub * per;
         q0 = max(0, r.ctx - w0);
-        q1 = mine ? min(w_rows, r.ctx + r.m - w0) : 0;
+        q1 = sound ? min(w_rows, r.ctx + r.m - w0) : 0;
         int page, slot, blk, rest2;
         pd.split(base, page, slot);
         bd.split(slot, blk, rest2);
-        const int id = table[page];
+        const int id = sound ? table[page] : 0;
         float* scale = P.scale[kv] + (long long)layer * P.c_layer + (long long)id * P.c_page + (long long)blk * P.c_block +
                        (long long)h * P.c_head;
         x = static_cast<const T*>(P.x[kv]) + (long long)layer * P.sn_layer + (long long)r.cu * P.sn_node +
             (long long)h * P.sn_head + ch;
         C8Unit& n = info[warp][slot_ahead];
-        const bool before = mine && base < r.ctx;
+        const bool before = sound && base < r.ctx;
         __syncwarp();  // its last unit has been read
         if (lane == 0) {
           n.scale = scale;
@@ -204,7 +268,7 @@ __global__ void __launch_bounds__(kC8Threads, D <= 128 ? 2 : 1) commit8_kernel(c
                    (long long)(slot + wsub * per) * P.s_slot + (long long)h * P.s_head;
           n.q0 = q0;
           n.q1 = q1;
-          n.flags = (mine ? 1 : 0) | (before ? 2 : 0);
+          n.flags = (sound ? 1 : 0) | (before ? 2 : 0);
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&n.old)), "l"(scale), "r"(before ? 4 : 0)
                        : "memory");
         }
@@ -220,7 +284,7 @@ __global__ void __launch_bounds__(kC8Threads, D <= 128 ? 2 : 1) commit8_kernel(c
       }
       if (++step_ahead == steps) {
         step_ahead = 0;
-        base_ahead += stride;
+        ++u_ahead;
       }
       if (++slot_ahead == S::kStages) slot_ahead = 0;
     }
@@ -241,7 +305,7 @@ __global__ void __launch_bounds__(kC8Threads, D <= 128 ? 2 : 1) commit8_kernel(c
     for (int i = 0; i < N; ++i) v[i] = lane_on ? *reinterpret_cast<const uint4*>(at + i * (R * D * 2)) : make_uint4(0u, 0u, 0u, 0u);
     if (++slot_now == S::kStages) slot_now = 0;
   };
-  for (long long u0 = u_base; u0 < units; u0 += stride, turn ^= 1) {
+  for (long long u = u_from; u < u_to; ++u, turn ^= 1) {
     C8Unit n;
     float* scale = nullptr;
     uint8_t* held = nullptr;  // row rsub
@@ -322,16 +386,23 @@ __global__ void __launch_bounds__(kC8Threads, D <= 128 ? 2 : 1) commit8_kernel(c
     }
     if (grown && lane_on) {  // tokens that were there, under the new scale
       uint8_t* d = held;
-      for (int q = rsub; q < min(w_rows, n.q0); q += R, d += row_step) {
-        const uint2 w = *reinterpret_cast<const uint2*>(d);
-        uint32_t z[2];
+      const int end = min(w_rows, n.q0);
+      constexpr int U = 4;  // loads in flight
+      for (int q = rsub; q < end; q += U * R, d += U * row_step) {
+        uint2 w[U];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t y = k ? w.y : w.x;
-          const float2 a = from_e4m3x2(y & 0xffffu), c = from_e4m3x2(y >> 16);
-          z[k] = to_e4m3x2(a.x * old * inv, a.y * old * inv) | to_e4m3x2(c.x * old * inv, c.y * old * inv) << 16;
+        for (int e = 0; e < U; ++e) w[e] = q + e * R < end ? *reinterpret_cast<const uint2*>(d + e * row_step) : make_uint2(0u, 0u);
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+          uint32_t z[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t y = k ? w[e].y : w[e].x;
+            const float2 a = from_e4m3x2(y & 0xffffu), c = from_e4m3x2(y >> 16);
+            z[k] = to_e4m3x2(a.x * old * inv, a.y * old * inv) | to_e4m3x2(c.x * old * inv, c.y * old * inv) << 16;
+          }
+          if (q + e * R < end) *reinterpret_cast<uint2*>(d + e * row_step) = make_uint2(z[0], z[1]);
         }
-        *reinterpret_cast<uint2*>(d) = make_uint2(z[0], z[1]);
       }
     }
   }
@@ -366,8 +437,7 @@ int launch_commit_dim(const Commit8Params& P, bool checked, dim3 grid, cudaStrea
   }
 }
 
-constexpr int kC8OwnCheck = 256;  // longest path that every CTA checks by itself
-constexpr int kC8Waves = 6;       // CTAs for each SM
+constexpr int kC8OwnCheck = 256;  // longest path that every group checks by itself
 
 }  // namespace
 
@@ -375,15 +445,12 @@ int launch_commit8(Commit8Params& P, bool bf16, int num_sms, cudaStream_t s) {
   const int need = (P.block + kC8Rows - 1) / kC8Rows;
   P.warps = 1;
   while (P.warps < kC8Warps && P.warps < need) P.warps *= 2;
-  const long long blocks = (P.ld_path + P.block - 2ll) / P.block + 1, units = blocks * P.heads * 2 * P.layers;
-  const int groups = kC8Warps / P.warps;
-  // As many CTAs as run at once, several times where there is work for them: a
-  // request's share depends on its path, which the host does not know.
-  const long long turns = (units + groups - 1) / groups, share = (kC8Waves * num_sms + P.B - 1) / P.B;
-  const unsigned y = (unsigned)(turns < share ? turns : share < 65535 ? share : 65535);
+  const long long blocks = (P.ld_path + P.block - 2ll) / P.block + 1, units = blocks * P.heads * 2 * P.layers * P.B;
+  const int groups = kC8Warps / P.warps, room = num_sms * (P.dim <= 128 ? 2 : 1);  // CTAs that run at once
+  const unsigned ctas = (unsigned)max(1ll, min((long long)room, (units + groups - 1) / groups));
   const bool checked = P.new_len == P.ctx || P.ld_path > kC8OwnCheck;
   if (checked && launch_kernel(commit8_check_kernel, dim3(P.B), kC8Threads, 0, s, P)) return -1;
-  const dim3 grid((unsigned)P.B, y);
+  const dim3 grid(ctas);
   return bf16 ? launch_commit_dim<__nv_bfloat16>(P, checked, grid, s) : launch_commit_dim<__half>(P, checked, grid, s);
 }
 
