@@ -1153,9 +1153,15 @@ bool encode8(CUtensorMap* m, const TreeParams& P, const void* base, int box) {
   cuuint64_t strides[3];
   for (int i = 0; i < 3; ++i) strides[i] = dims[i + 1] == 1 ? 512 : (cuuint64_t)st[i];
   const cuuint32_t bx[4] = {(cuuint32_t)P.dim, (cuuint32_t)box, 1, 1}, one[4] = {1, 1, 1, 1};
+  // What a miss brings to L2: not more than a row, unless the rows of a head lie
+  // together.  With 256 bytes, 128 K tokens of 8 heads cost 735 MB of DRAM reads
+  // for 482.
+  const CUtensorMapL2promotion promotion = P.s_slot == P.dim ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                           : P.dim == 64     ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                                             : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
   return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, bx, one,
            CU_TENSOR_MAP_INTERLEAVE_NONE, P.dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+           promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename T, int D, int ROWS>

@@ -118,15 +118,16 @@ int check_cache8_args(const spec_cache8_args* a, spec_tree_args* t) {
 }
 
 // The tensor-memory kernel takes the calls whose tiles TMA can copy, with a
-// positive scale, and more query rows per key head than one warp tile holds.
-constexpr int kWarpRows8 = 16;
-
+// positive scale, down to one token of one request: against warp tiles, 64
+// requests of one token over up to 8192, 28 / 4 heads of 128 channels, 125 us and
+// 160; one of 2000 tokens, 32 / 8 heads, 23 and 28; one of 1001 tokens, 14 / 2
+// heads of 64, 12.3 and 12.0.
 sv::TreePlan plan_cache8(const spec_cache8_args* a, int num_sms) {
   const spec_cache8& c = a->cache;
   const int rows = a->max_nodes * (a->heads_q / c.heads);
   const bool fits = rows <= kMaxTcRows && a->scale > 0.f && sv::cache8_tc_fits(c.dim, c.page_size, c.block) && a->total_nodes > 0 &&
                     tma_stride(c.s_slot, c.page_size) && tma_stride(c.s_head, c.heads) && tma_stride(c.s_page, c.num_pages);
-  return fits && rows > kWarpRows8 ? sv::plan_cache8_tc(rows, num_sms) : sv::plan_cache8_warp(c.dim, num_sms);
+  return fits ? sv::plan_cache8_tc(rows, num_sms) : sv::plan_cache8_warp(c.dim, num_sms);
 }
 
 // The largest power of two up to 64 that divides the page size: the copies of
