@@ -121,6 +121,13 @@ __device__ __forceinline__ uint32_t max_size2<__nv_bfloat16>(uint32_t a, uint32_
 // CHECKED: the check kernel has run, and a new length of -1 says that the
 // request is bad.  Otherwise every group checks the requests of its units, and
 // the one with a request's first unit tells the caller.
+//
+// Prompts of up to 4096 tokens, 16 layers of 8 heads, take 414 us (6.1 TB/s, 90 % of
+// the copy rate); the paths of 64 requests, 28 layers of 4 heads, 27.5 (2.4 TB/s):
+// there the start (lengths, path, table, rows, each after the one before) takes a
+// third, and a unit of few rows costs what its lookups and scale cost.  CTAs of one
+// request each took 498 and 29.5; three CTAs an SM, whose registers spill, 630 and
+// 39.
 template <int D>
 struct C8Stage {
   static constexpr int kBytes = kC8Rows * D * 2;               // of a warp's step
@@ -437,7 +444,10 @@ int launch_commit_dim(const Commit8Params& P, bool checked, dim3 grid, cudaStrea
   }
 }
 
-constexpr int kC8OwnCheck = 256;  // longest path that every group checks by itself
+// Longest path that every group checks by itself.  A launch that checks first costs
+// 2.2 us (one request 5.4 to 7.6, the batch 27.5 to 29.0); checking prompts of 4096
+// tokens over and over 5 (414 to 419).
+constexpr int kC8OwnCheck = 256;
 
 }  // namespace
 

@@ -15,9 +15,7 @@ constexpr int kRows8 = 128;       // query rows per tile (lanes of tensor memory
 constexpr float kLazy8 = 8.f;
 constexpr float kTop8 = 7.f;
 
-// PAIR: two row tiles share every staged tile.  Otherwise one row tile's keys are
-// dealt out to two streams, tile by tile, each with scores, outputs and a running
-// reference of its own, joined at a segment's end.
+// PAIR: two row tiles share every staged tile.
 template <int D, bool PAIR>
 struct C8Shape {
   static constexpr int kQBytes = kRows8 * D * 2;
@@ -192,21 +190,43 @@ __device__ __forceinline__ float4 c8_scale(float ks, float vs) {
   return make_float4(ks, log2f(v), v == v ? 1.f / v : 0.f, vs < kLeastScale ? 1.f : 0.f);
 }
 
-// Warps 0 - 7: one query row a thread (the softmax); 8 - 11: conversion; 12 and
-// 15: copies of keys and of values; 13 and 14: products of each stream.
+// Warps 0 - 7: the softmax; 8 and 9 convert keys, 10 and 11 values; 12 and 15 copy
+// keys and values; 13 and 14 issue the products of each stream.
 //
 // The copying warps alone walk over the CTA's tiles.  They look up the pages of
 // four of them at once, a lane 16 keys, while the four before are copied, and the
 // first of them describes each tile and segment to the others.
 //
-// A tile of 128 keys comes as 8 bits (half the bytes of 16, which is what bounds
-// few rows); the conversion writes it in the swizzled layout that the products
-// read, a thread two keys.  Drafted keys and values are read from where they are
-// and scaled by 16 to be exact in fp16.  Per stream and unit of 64 keys:
-//   S = Q K^T (shared memory), y = ks S + log2 vs, the softmax by the row's
-//   thread, P = 2^(y - m) in fp16 over the scores read, O += P V (P from tensor
-//   memory), l += P / vs,
-// the products of one half running during the softmax of the other.
+// A tile of 128 keys comes as 8 bits; the conversion writes it in fp16 in the
+// swizzled layout that the products read, a thread a key's row in two steps.
+// Drafted keys and values are read from where they are, 16 keys a warp, and
+// scaled to be exact in fp16.  Per stream and tile:
+//   S = Q K^T (shared memory), y = ks S + log2 vs, the softmax by rows,
+//   P = 2^(y - m) in fp16 over the scores read, O += P V (P from tensor memory),
+//   l += P / vs.
+//
+// ROWS, the query rows of a key head that a CTA takes at once:
+// - 256: two tiles of 128 rows share the staged keys, each a stream of its own, a
+//   thread a row, by halves of a tile.
+// - 128: one tile of rows, whose tiles of keys two streams take in turn, each with
+//   scores, outputs and reference of its own, joined at a segment's end.
+// - 64: as 128, with products of 64 rows, which lie in 16 lanes of each warp's
+//   32.  A thread then has half of the keys of two rows in the layout of a matrix
+//   fragment, so all eight warps are at work where 128 rows would leave half of
+//   them idle.
+// 16 requests with trees over up to 16384 tokens, 32 / 8 heads, cold: 16 nodes (64
+// rows) 109 / 117 / 139 us with ROWS 64 / 128 / 256, 32 nodes 117 and 143 with 128
+// and 256, 64 nodes 217 and 166.
+//
+// 64 ragged requests of up to 9 nodes over up to 8192 tokens take 120 us, trees of
+// up to 64 nodes over up to 16384 159, two requests over 128 K tokens 132 (54 % of
+// the copy rate).  A tile moves 208 KB through shared memory (32 written by the
+// copies, 32 read and 64 written by the conversion, 80 read by the products; 224
+// with more than 64 rows), 1650 cycles at 128 bytes a cycle, and takes some 2400:
+// the conversion works for 1500 of them and waits for copies and free slots for
+// the rest.  Products on the bytes themselves, with queries in three e4m3 parts,
+// took 195, 327 and 183 us.  A segment's end and the next one's queries cost some 20
+// thousand cycles, which is what short contexts have besides.
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kC8TcThreads, 1)
     cache8_tc_kernel(const Cache8Params C, const __grid_constant__ C8Maps maps, int box) {
@@ -542,9 +562,9 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
     mbar_wait(&fin[w], 0);  // every product has ended before tensor memory is freed
   } else if (warp >= kC8Softmax) {
     // -------------------------------------------------------- conversion
-    // Two warps convert keys and two values, a thread two keys of every tile: each
-    // pair of warps waits, fences and arrives once a tile, and neither waits for
-    // the other.
+    // Two warps convert keys and two values, a thread two keys' rows of every tile:
+    // each pair waits, fences and arrives once a tile, and neither waits for the
+    // other.
     const int kv = (warp - kC8Softmax) >> 1, row0 = ((warp & 1) << 5) + lane;
     const uint32_t em = exp_mask<T>();
     bool ok = true;
@@ -1155,7 +1175,7 @@ bool encode8(CUtensorMap* m, const TreeParams& P, const void* base, int box) {
   const cuuint32_t bx[4] = {(cuuint32_t)P.dim, (cuuint32_t)box, 1, 1}, one[4] = {1, 1, 1, 1};
   // What a miss brings to L2: not more than a row, unless the rows of a head lie
   // together.  With 256 bytes, 128 K tokens of 8 heads cost 735 MB of DRAM reads
-  // for 482.
+  // for 491.
   const CUtensorMapL2promotion promotion = P.s_slot == P.dim ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
                                            : P.dim == 64     ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
                                                              : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;

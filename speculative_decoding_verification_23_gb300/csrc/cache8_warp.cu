@@ -43,6 +43,11 @@ __device__ __forceinline__ uint32_t without_nan8(uint32_t w, bool& any) {
 // channels is the threads' own: a thread reads 8 bytes of a key for two steps of
 // 16 channels, and 4 channels of 4 keys for the values, whose bytes it pairs by
 // key before they are converted, so neither needs a transposition.
+//
+// It serves the calls that the tensor-memory kernel does not take.  64 requests of
+// one token over up to 8192 tokens, 28 / 4 heads of 128, would take 160 us (125
+// there), and 9 nodes of them, five row tiles that read the keys anew, 470: the
+// conversions and products of few rows bound it, not the copies.
 template <typename T, int D>
 __global__ void __launch_bounds__(kW8Warps * 32, W8Shape<D>::kCtas) cache8_warp_kernel(const Cache8Params C) {
   using S = W8Shape<D>;

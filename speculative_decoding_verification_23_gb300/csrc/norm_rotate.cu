@@ -57,12 +57,17 @@ struct Run {
 // (channels CH l .. and rot / 2 more), so only the mean crosses lanes, and a warp
 // up to 8 heads of a row at once.  It walks over the row's heads with the row's
 // sines and cosines in registers, which the lanes of the same channels compute
-// together.  CH is 8 (16-byte accesses) where rot is a multiple of 16, else 4.
+// together.  CH is 8 (16-byte accesses) where rot is a multiple of 16, else 4:
+// 16384 rows of 32 heads of 128 take 55 us with 8 and 68 with 4.
 //
 // The angle in turns is positions[r] f_i / 2 pi.  Its fraction is exact in
 // 64-bit fixed point: F_i = frac(f_i / 2 pi) 2^64 once per CTA, in fp64, and
 // the fraction of position times F_i is the low 64 bits of the product of
 // whole numbers.  In fp32 a position of 2^17 leaves 7 bits of the turn.
+//
+// Bytes bound it, 2 read and 2 written a channel: 55 us are 4.9 TB/s, 72 % of the
+// copy rate, half of the traffic writes; one row of 16 heads takes 6.9 us, a
+// launch and two dependent loads.
 template <typename T, int D, int CH>
 __global__ void __launch_bounds__(kRotWarps * 32) norm_rotate_kernel(const RotateParams P) {
   constexpr int G = kRotLanes<D, CH>, H = 32 / G;
@@ -195,7 +200,9 @@ __global__ void __launch_bounds__(kRotWarps * 32) norm_rotate_kernel(const Rotat
   }
 }
 
-constexpr int kRotCtas = 2;  // per SM
+// CTAs per SM: with 1, 2, 3 and 4 the 16384 rows take 82, 55, 66 and 57 us (a row's
+// sines are computed once per warp, and 3 do not run at once).
+constexpr int kRotCtas = 2;
 
 template <typename T, int D, int CH>
 int launch(RotateParams& P, int num_sms, cudaStream_t s) {
