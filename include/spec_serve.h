@@ -111,8 +111,9 @@ typedef struct {
  *
  * Products run on fp16 operands that hold the bytes' values, and queries and
  * drafted keys and values, exactly: bf16 rows are scaled by powers of two
- * first, and what is below 2^-32 of a query row's largest value, or of the
- * largest value of 16 drafted keys, is rounded to 2^-40 of it.  Weights, times
+ * first, and what is below 2^-31 of a query row's largest finite size, or of that
+ * of 16 drafted keys or values, is rounded within 2^-39 of it (of sizes below
+ * 2^-46, within 2^-85).  Weights, times
  * the scale of their values, are rounded to fp16 relative to the row's largest
  * such product (at least 2^6 of 2^16, smallest step 2^-24), so with p_j =
  * exp(s_j - lse) an output is off by at most 2^-11 (1 + 2^-19) sum_j p_j |v_j|

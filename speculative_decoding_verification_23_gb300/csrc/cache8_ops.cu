@@ -122,12 +122,13 @@ __device__ __forceinline__ uint32_t max_size2<__nv_bfloat16>(uint32_t a, uint32_
 // request is bad.  Otherwise every group checks the requests of its units, and
 // the one with a request's first unit tells the caller.
 //
-// Prompts of up to 4096 tokens, 16 layers of 8 heads, take 414 us (6.1 TB/s, 90 % of
+// Prompts of up to 4096 tokens, 16 layers of 8 heads, take 416 us (6.1 TB/s, 90 % of
 // the copy rate); the paths of 64 requests, 28 layers of 4 heads, 27.5 (2.4 TB/s):
 // there the start (lengths, path, table, rows, each after the one before) takes a
 // third, and a unit of few rows costs what its lookups and scale cost.  CTAs of one
 // request each took 498 and 29.5; three CTAs an SM, whose registers spill, 630 and
-// 39.
+// 39.  Every CTA adds up the units of all requests, a thread each: 1024 requests of
+// such paths over 4 layers take 61 us, 90 when each warp does so by itself.
 template <int D>
 struct C8Stage {
   static constexpr int kBytes = kC8Rows * D * 2;               // of a warp's step
@@ -153,11 +154,13 @@ __global__ void __launch_bounds__(kC8Threads, D <= 128 ? 2 : 1) commit8_kernel(c
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float tops[2][kC8Warps];
   __shared__ C8Unit info[kC8Warps][S::kStages];
+  __shared__ long long warp_units[kC8Warps];
+  long long* before = reinterpret_cast<long long*>(smem);  // of each thread, until rows are copied there
   after_previous();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const PageDiv pd(P.page_size), bd(P.block);
   const int W = P.warps, group = warp / W, wsub = warp % W, groups = kC8Warps / W;
-  // Requests: their units, and a lane's sum of those of its requests.
+  // Requests: their units, and those before each thread's requests.
   Path8 r;
   int first_block = 0, of_layer = 0;  // heads change first: neighbours' rows lie side by side
   auto request = [&](int b) {         // returns the units
@@ -178,43 +181,54 @@ __global__ void __launch_bounds__(kC8Threads, D <= 128 ? 2 : 1) commit8_kernel(c
     of_layer = (last_block - first_block + 1) * P.heads * 2;
     return (long long)of_layer * P.layers;
   };
-  const int per_lane = (P.B + 31) / 32;
+  const int per_thread = (P.B + kC8Threads - 1) / kC8Threads;
   long long mine = 0;
-  for (int b = lane * per_lane; b < min(P.B, (lane + 1) * per_lane); ++b) {
+  for (int b = tid * per_thread; b < min(P.B, (tid + 1) * per_thread); ++b) {
     const long long units = request(b);
     mine += units;
-    if (!CHECKED && units == 0 && blockIdx.x == 0 && warp == 0) {  // nothing to write, or bad
+    if (!CHECKED && units == 0 && blockIdx.x == 0) {  // nothing to write, or bad
       const int status = path_status(r.m == 0, 0);
       if (P.status) P.status[b] = status;
       P.new_len[b] = status ? -1 : r.ctx;
     }
   }
-  long long before = mine;
+  long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += x;
+    const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
   }
-  const long long total = __shfl_sync(0xffffffffu, before, 31), all = (long long)gridDim.x * groups;
-  before -= mine;
-  const long long at_group = (long long)blockIdx.x * groups + group;
+  if (lane == 31) warp_units[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+  for (int w = 0; w < kC8Warps; ++w) {
+    if (w == warp) before[tid] = total + upto - mine;
+    total += warp_units[w];
+  }
+  __syncthreads();
+  const long long all = (long long)gridDim.x * groups, at_group = (long long)blockIdx.x * groups + group;
   const long long u_from = div_fast(at_group * total, all), u_to = div_fast((at_group + 1) * total, all);
-  if (u_from == u_to) return;  // every warp of the group
   // The request of the first unit.
   int b = 0;
-  long long first = before;
-  {
-    const bool me = u_from >= before && u_from < before + mine;
-    if (me)
-      for (b = lane * per_lane;; ++b) {
+  long long first = 0;
+  if (u_from < u_to) {
+    int own = -1;  // the thread with it
+    for (int i = lane; i < kC8Threads; i += 32)
+      if (u_from >= before[i] && u_from < (i + 1 < kC8Threads ? before[i + 1] : total)) own = i;
+    if (own >= 0) {
+      first = before[own];
+      for (b = own * per_thread;; ++b) {
         const long long units = request(b);
         if (u_from < first + units) break;
         first += units;
       }
-    const int src = __ffs(__ballot_sync(0xffffffffu, me)) - 1;
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, own >= 0)) - 1;
     b = __shfl_sync(0xffffffffu, b, src);
     first = __shfl_sync(0xffffffffu, first, src);
   }
+  __syncthreads();
+  if (u_from == u_to) return;  // every warp of the group
   long long units = request(b);
   const int32_t* path = nullptr;
   const int32_t* table = nullptr;
@@ -267,7 +281,7 @@ __global__ void __launch_bounds__(kC8Threads, D <= 128 ? 2 : 1) commit8_kernel(c
         x = static_cast<const T*>(P.x[kv]) + (long long)layer * P.sn_layer + (long long)r.cu * P.sn_node +
             (long long)h * P.sn_head + ch;
         C8Unit& n = info[warp][slot_ahead];
-        const bool before = sound && base < r.ctx;
+        const bool begun = sound && base < r.ctx;
         __syncwarp();  // its last unit has been read
         if (lane == 0) {
           n.scale = scale;
@@ -275,8 +289,8 @@ __global__ void __launch_bounds__(kC8Threads, D <= 128 ? 2 : 1) commit8_kernel(c
                    (long long)(slot + wsub * per) * P.s_slot + (long long)h * P.s_head;
           n.q0 = q0;
           n.q1 = q1;
-          n.flags = (sound ? 1 : 0) | (before ? 2 : 0);
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&n.old)), "l"(scale), "r"(before ? 4 : 0)
+          n.flags = (sound ? 1 : 0) | (begun ? 2 : 0);
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&n.old)), "l"(scale), "r"(begun ? 4 : 0)
                        : "memory");
         }
       }
@@ -316,7 +330,7 @@ __global__ void __launch_bounds__(kC8Threads, D <= 128 ? 2 : 1) commit8_kernel(c
     C8Unit n;
     float* scale = nullptr;
     uint8_t* held = nullptr;  // row rsub
-    bool before = false;
+    bool begun = false;
     uint32_t top = 0;  // of two values at once
     bool odd = false;  // infinities
 #pragma unroll 1
@@ -327,7 +341,7 @@ __global__ void __launch_bounds__(kC8Threads, D <= 128 ? 2 : 1) commit8_kernel(c
         n = info[warp][slot];
         scale = n.scale;
         held = n.held + (long long)rsub * P.s_slot + ch;
-        before = (n.flags & 2) != 0;
+        begun = (n.flags & 2) != 0;
       }
       copy();  // into the slot that the step before left
       uint32_t size = 0;
@@ -358,9 +372,9 @@ __global__ void __launch_bounds__(kC8Threads, D <= 128 ? 2 : 1) commit8_kernel(c
     }
     const float need = scale_for(big);
     const float old = n.old;
-    const bool grown = before && need > old;
-    const float s = before && !grown ? old : need, inv = s == 0.f ? 0.f : 1.f / s;
-    if ((n.flags & 1) && wsub == 0 && lane == 0 && (!before || grown)) *scale = s;
+    const bool grown = begun && need > old;
+    const float s = begun && !grown ? old : need, inv = s == 0.f ? 0.f : 1.f / s;
+    if ((n.flags & 1) && wsub == 0 && lane == 0 && (!begun || grown)) *scale = s;
     // eight values under the scale
     auto bytes8 = [&](const uint4& x, bool odd) {
       const uint32_t e[4] = {x.x, x.y, x.z, x.w};

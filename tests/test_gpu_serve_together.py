@@ -11,7 +11,8 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 import serve_ref as ref  # noqa: E402
 import speculative_decoding_verification_23_gb300 as sv  # noqa: E402
-from test_gpu_serve import DEV, DT, Case, gen, i32, normal, same_bytes, trees  # noqa: E402
+from test_gpu_serve import (DEV, DT, Case, commit_args, commit_case, commit_want, gen, i32, normal, same_bytes,  # noqa: E402
+                            trees)
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
@@ -256,6 +257,23 @@ def test_attention_past_32_bit_offsets():
     table = np.where(small.table >= 0, small.table + pages - n, small.table)
     small.k, small.v, small.scales, small.table = k, v, [ks, vs], table
     assert torch.equal(small.run()[0], want)
+
+
+@pytest.mark.parametrize("B", [31, 257, 700])
+def test_commitment_of_many_requests(B):
+    """More requests than threads that add them up; some without tokens, some bad."""
+    rng = np.random.RandomState(B)
+    ctx, nodes = rng.randint(0, 70, B).tolist(), rng.randint(1, 4, B).tolist()
+    c = commit_case(dtype="bf16", layers=2, kv=1, dim=64, page=16, block=8, ctx=ctx, nodes=nodes,
+                    accepted=[int(rng.randint(0, n + 1)) for n in nodes], seed=B)
+    want = commit_want({**c, "m": np.where(np.arange(B) % 7 == 3, 0, c["m"])})
+    bad = (np.arange(B) % 7 == 3) & (c["m"] > 0)
+    c["path"][bad, 0] = 300      # no such node: nothing of the request is written
+    length, status = sv.spec_cache8_commit(commit_args(c))
+    assert status.tolist() == np.where(bad, sv.SPEC_STATUS_BAD_LEN, 0).tolist()
+    assert length.tolist() == np.where(bad, -1, c["ctx"] + c["m"]).tolist()
+    for x, s, (held, scale) in zip((c["k"], c["v"]), (c["ks"], c["vs"]), want):
+        assert same_bytes(x, held) and np.array_equal(s.cpu().numpy(), scale)
 
 
 @pytest.mark.parametrize("dim,group,nodes", [(128, 4, 64), (64, 8, 40), (128, 2, 30), (128, 2, 60), (64, 2, 50), (64, 1, 17)])
