@@ -288,6 +288,39 @@ def test_many_tiles_give_the_same_bits_again(dim, group, nodes):
         assert all(torch.equal(x, y) for x, y in zip(c.run(args), want))
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("block", [None, 16, 32])
+def test_caches_of_other_layouts(dim, block):
+    """A head's tokens side by side; and some heads of a wider cache, whose results are those of a copy of them."""
+    kw = dict(dtype="bf16", dim=dim, kv=3, group=4, page=32, ctx=[700, 45, 32], nodes=[9, 17, 1], chain=False,
+              window=None if block else 150, sinks=0 if block else 33, block=block, seed=9)
+    Case(layout="phsd", **kw).check()
+    c = Case(**kw)
+    want = c.run()
+    wide = [torch.empty(*x.shape[:2], 5, dim, dtype=x.dtype, device=DEV) for x in (c.k, c.v)]
+    for w, x in zip(wide, (c.k, c.v)):
+        w.view(torch.uint8).fill_(0x7f)     # NaN around them
+        w[:, :, 1:4].copy_(x)
+    c.k, c.v = (w[:, :, 1:4] for w in wide)
+    if block:
+        scales = [torch.full((*s.shape[:2], 5), float("nan"), device=DEV) for s in c.scales]
+        for w, s in zip(scales, c.scales):
+            w[..., 2:5].copy_(s)
+        c.scales = [w[..., 2:5] for w in scales]
+    assert all(torch.equal(x, y) for x, y in zip(c.run(), want))
+
+
+def test_queries_and_drafted_tokens_of_one_projection():
+    """Strided queries, keys and values, each a part of the same rows."""
+    for block, nodes in ((None, [5, 40]), (16, [5, 40]), (16, [2, 3])):
+        c = Case(dtype="fp16", dim=128, kv=2, group=4, page=16, ctx=[130, 700], nodes=nodes, chain=True,
+                 window=None if block else 90, block=block, seed=12)
+        want = c.run()
+        rows = torch.full((c.q.shape[0], 13, 128), float("nan"), dtype=torch.float16, device=DEV)
+        rows[:, :8], rows[:, 8:10], rows[:, 11:] = c.q, c.k_new, c.v_new
+        assert all(torch.equal(x, y) for x, y in zip(c.run(c.args(q=rows[:, :8], k_new=rows[:, 8:10], v_new=rows[:, 11:])), want))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("window", [None, 130])
 @pytest.mark.parametrize("dim,group,nodes", [(128, 1, (17, 31)), (128, 2, (32, 9)), (64, 1, (33, 64)), (128, 1, (65, 3)),
