@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
     auto issue = [&](const Batch& x) {
       // a lane's part in its tile's copy: the first of each box's keys
       const bool mine = key < x.d.valid() && (key & (box - 1)) == 0;
+      __syncwarp();  // lanes may leave the lookup one by one
       const bool any_bad = !values && __any_sync(0xffffffffu, x.e.bad != 0);
 #pragma unroll 1
       for (int i = 0; ok && i < x.count; ++i, ++tc) {
