@@ -214,12 +214,15 @@ __device__ __forceinline__ float4 c8_scale(float ks, float vs) {
 //   32.  A thread then has half of the keys of two rows in the layout of a matrix
 //   fragment, so all eight warps are at work where 128 rows would leave half of
 //   them idle.
+//   The softmax goes by halves of a tile, whose products begin as soon as its
+//   weights are there; by whole tiles the chains below take 120 us for 114, the
+//   long contexts 132 for 134.
 // 16 requests with trees over up to 16384 tokens, 32 / 8 heads, cold: 16 nodes (64
 // rows) 109 / 117 / 139 us with ROWS 64 / 128 / 256, 32 nodes 117 and 143 with 128
 // and 256, 64 nodes 217 and 166.
 //
-// 64 ragged requests of up to 9 nodes over up to 8192 tokens take 120 us, trees of
-// up to 64 nodes over up to 16384 159, two requests over 128 K tokens 132 (54 % of
+// 64 ragged requests of up to 9 nodes over up to 8192 tokens take 114 us, trees of
+// up to 64 nodes over up to 16384 159, two requests over 128 K tokens 134 (54 % of
 // the copy rate).  A tile moves 208 KB through shared memory (32 written by the
 // copies, 32 read and 64 written by the conversion, 80 read by the products; 224
 // with more than 64 rows), 1650 cycles at 128 bytes a cycle, and takes some 2400:
@@ -510,12 +513,10 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
         ok = ok && warp_wait(&h_full[v_slot], v_ph);
 #pragma unroll 1
         for (int h = 0; ok && h * kUnit8 < n16; ++h) {
-          if (!HALF || h == 0) {
-            ok = warp_wait(&p_ready[w * 2 + h], (p_ph >> h) & 1);
-            if (!ok) break;
-            p_ph ^= 1u << h;
-            tc_fence_after();
-          }
+          ok = warp_wait(&p_ready[w * 2 + h], (p_ph >> h) & 1);
+          if (!ok) break;
+          p_ph ^= 1u << h;
+          tc_fence_after();
           const uint64_t db = dv + (uint32_t)(v_slot * (S::kSlot >> 4) + h * (4 * 2048 >> 4));
           const uint32_t at = p + h * kUnit8, begun = h > 0 || i > first;
           const int steps = min(4, n16 / 16 - h * 4);
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
 #pragma unroll 1
             for (int ks = 0; ks < steps; ++ks) mma_ts(o, at + ks * 8, db + ks * (2048 >> 4), id_v, ks > 0 || begun, one);
           }
-          if (!HALF && h == 0) mma_commit(&o_half[w], one);
+          if (h == 0) mma_commit(&o_half[w], one);
           if ((h + 1) * kUnit8 >= n16) {
             mma_commit(&o_done[w], one);  // before the scores that the softmax takes for a sign of it
             mma_commit(&h_empty[v_slot], one);
@@ -835,106 +836,107 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
           if (!ok) break;
         }
         if constexpr (HALF) {
-          ok = warp_wait(&s_full[w * 2], s_ph);
-          s_ph ^= 1u;
-          if (!ok) break;
-          tc_fence_after();
-          if (any) {
-            const uint32_t s_at = tmem + lanes + w * kTcKeys;
-            float z[kTcKeys / 2];  // of eight keys: two of row a, two of row b
-            tmem_ld_pairs(s_at, z);
-            tmem_ld_pairs(s_at + 64, z + 32);
-            const float4* sc = scales[at];
-            tmem_wait_ld();
-            loaded(z);
-            loaded(z + 32);
-#pragma unroll
-            for (int q = 0; q < kTcKeys / 16; ++q) {
-              const float4 e4 = sc[q];
-              const float2 ca = make_float2(e4.x * rsc_a, e4.x * rsc_a), cb = make_float2(e4.x * rsc_b, e4.x * rsc_b);
-              const float2 b2 = make_float2(e4.y, e4.y);
-#pragma unroll
-              for (int k = q * 8; k < q * 8 + 8; k += 4) {
-                const float2 a = __ffma2_rn(make_float2(z[k], z[k + 1]), ca, b2), b = __ffma2_rn(make_float2(z[k + 2], z[k + 3]), cb, b2);
-                z[k] = a.x;
-                z[k + 1] = a.y;
-                z[k + 2] = b.x;
-                z[k + 3] = b.y;
-              }
-            }
-            if (masked) {  // -inf where the row sees nothing
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const int rest = valid - c * 32;
-                uint32_t bits = rest >= 32 ? 0xffffffffu : (rest <= 0 ? 0u : (1u << rest) - 1u);
-                if (x.some()) bits &= see[c];
-                const uint32_t ba = __shfl_sync(0xffffffffu, bits, src_a) >> pair, bb = __shfl_sync(0xffffffffu, bits, src_b) >> pair;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                  for (int j = 0; j < 2; ++j) {
-                    float* y = z + c * 16 + k * 4 + j;
-                    y[0] = (ba >> (k * 8 + j)) & 1u ? y[0] : -INFINITY;
-                    y[2] = (bb >> (k * 8 + j)) & 1u ? y[2] : -INFINITY;
-                  }
-              }
-            }
-            float ta[2], tb[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              ta[k] = fmaxf(z[4 * k], z[4 * k + 1]);
-              tb[k] = fmaxf(z[4 * k + 2], z[4 * k + 3]);
-            }
-#pragma unroll
-            for (int q = 8; q < kTcKeys / 2; q += 8)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                ta[k] = fmaxf(fmaxf(ta[k], z[q + 4 * k]), z[q + 4 * k + 1]);
-                tb[k] = fmaxf(fmaxf(tb[k], z[q + 4 * k + 2]), z[q + 4 * k + 3]);
-              }
-            float za = fmaxf(ta[0], ta[1]), zb = fmaxf(tb[0], tb[1]);
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-              za = fmaxf(za, __shfl_xor_sync(0xffffffffu, za, o));
-              zb = fmaxf(zb, __shfl_xor_sync(0xffffffffu, zb, o));
-            }
-            const bool move_a = za > m + kLazy8 || (m == -INFINITY && za > -INFINITY);
-            const bool move_b = zb > m_b + kLazy8 || (m_b == -INFINITY && zb > -INFINITY);
-            if (__any_sync(0xffffffffu, move_a || move_b)) {
-              const float fa = move_a ? (m == -INFINITY ? 0.f : ex2(m - za)) : 1.f;
-              const float fb = move_b ? (m_b == -INFINITY ? 0.f : ex2(m_b - zb)) : 1.f;
-              m = move_a ? za : m;
-              m_b = move_b ? zb : m_b;
-              l2.x *= fa;
-              l2.y *= fa;
-              l3.x *= fb;
-              l3.y *= fb;
-              if (i > first) {
-                ok = warp_wait(&o_done[w], (mine_tc - 1) & 1);
-                if (!ok) break;
-                __syncwarp();
-                tc_fence_after();
-                const float f = of_row(fa, fb);
 #pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                  uint32_t o[16];
-                  tmem_ld16(o_at + c * 16, o);
+          for (int h = 0; h * kUnit8 < n16; ++h) {
+            if (h == 0) {  // of both halves
+              ok = warp_wait(&s_full[w * 2], s_ph);
+              s_ph ^= 1u;
+              if (!ok) break;
+              tc_fence_after();
+            }
+            if (any) {
+              const uint32_t s_at = tmem + lanes + w * kTcKeys + h * kUnit8;
+              float z[kUnit8 / 2];  // of eight keys: two of row a, two of row b
+              tmem_ld_pairs(s_at, z);
+              const float4* sc = &scales[at][h * 4];
+              tmem_wait_ld();
+              loaded(z);
 #pragma unroll
-                  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                  tmem_st16(o_at + c * 16, o);
+              for (int q = 0; q < kUnit8 / 16; ++q) {
+                const float4 e4 = sc[q];
+                const float2 ca = make_float2(e4.x * rsc_a, e4.x * rsc_a), cb = make_float2(e4.x * rsc_b, e4.x * rsc_b);
+                const float2 b2 = make_float2(e4.y, e4.y);
+#pragma unroll
+                for (int k = q * 8; k < q * 8 + 8; k += 4) {
+                  const float2 a = __ffma2_rn(make_float2(z[k], z[k + 1]), ca, b2), b = __ffma2_rn(make_float2(z[k + 2], z[k + 3]), cb, b2);
+                  z[k] = a.x;
+                  z[k + 1] = a.y;
+                  z[k + 2] = b.x;
+                  z[k + 3] = b.y;
                 }
               }
-            }
-            const float ref_a = m == -INFINITY ? 0.f : m - kTop8, ref_b = m_b == -INFINITY ? 0.f : m_b - kTop8;
-            const float2 na = make_float2(-ref_a, -ref_a), nb = make_float2(-ref_b, -ref_b);
+              if (masked) {  // -inf where the row sees nothing
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < 2; ++c) {
+                  const int rest = valid - h * kUnit8 - c * 32;
+                  uint32_t bits = rest >= 32 ? 0xffffffffu : (rest <= 0 ? 0u : (1u << rest) - 1u);
+                  if (x.some()) bits &= h == 0 ? see[c] : see[2 + c];
+                  const uint32_t ba = __shfl_sync(0xffffffffu, bits, src_a) >> pair, bb = __shfl_sync(0xffffffffu, bits, src_b) >> pair;
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                      float* y = z + c * 16 + k * 4 + j;
+                      y[0] = (ba >> (k * 8 + j)) & 1u ? y[0] : -INFINITY;
+                      y[2] = (bb >> (k * 8 + j)) & 1u ? y[2] : -INFINITY;
+                    }
+                }
+              }
+              float ta[2], tb[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                ta[k] = fmaxf(z[4 * k], z[4 * k + 1]);
+                tb[k] = fmaxf(z[4 * k + 2], z[4 * k + 3]);
+              }
+#pragma unroll
+              for (int q = 8; q < kUnit8 / 2; q += 8)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  ta[k] = fmaxf(fmaxf(ta[k], z[q + 4 * k]), z[q + 4 * k + 1]);
+                  tb[k] = fmaxf(fmaxf(tb[k], z[q + 4 * k + 2]), z[q + 4 * k + 3]);
+                }
+              float za = fmaxf(ta[0], ta[1]), zb = fmaxf(tb[0], tb[1]);
+#pragma unroll
+              for (int o = 1; o < 4; o <<= 1) {
+                za = fmaxf(za, __shfl_xor_sync(0xffffffffu, za, o));
+                zb = fmaxf(zb, __shfl_xor_sync(0xffffffffu, zb, o));
+              }
+              const bool move_a = za > m + kLazy8 || (m == -INFINITY && za > -INFINITY);
+              const bool move_b = zb > m_b + kLazy8 || (m_b == -INFINITY && zb > -INFINITY);
+              if (__any_sync(0xffffffffu, move_a || move_b)) {
+                const float fa = move_a ? (m == -INFINITY ? 0.f : ex2(m - za)) : 1.f;
+                const float fb = move_b ? (m_b == -INFINITY ? 0.f : ex2(m_b - zb)) : 1.f;
+                m = move_a ? za : m;
+                m_b = move_b ? zb : m_b;
+                l2.x *= fa;
+                l2.y *= fa;
+                l3.x *= fb;
+                l3.y *= fb;
+                if (i > first || h > 0) {  // as below
+                  if (mine_tc > 0) ok = warp_wait(&o_done[w], (mine_tc - 1) & 1);
+                  if (h > 0) ok = ok && warp_wait(&o_half[w], mine_tc & 1);
+                  if (!ok) break;
+                  __syncwarp();
+                  tc_fence_after();
+                  const float f = of_row(fa, fb);
+#pragma unroll 1
+                  for (int c = 0; c < D / 16; ++c) {
+                    uint32_t o[16];
+                    tmem_ld16(o_at + c * 16, o);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st16(o_at + c * 16, o);
+                  }
+                }
+              }
+              const float ref_a = m == -INFINITY ? 0.f : m - kTop8, ref_b = m_b == -INFINITY ? 0.f : m_b - kTop8;
+              const float2 na = make_float2(-ref_a, -ref_a), nb = make_float2(-ref_b, -ref_b);
               uint32_t p[16];
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const float iv = sc[c * 4 + k / 2].z;
+                const float iv = sc[k / 2].z;
                 const float2 i2 = make_float2(iv, iv);
-                const float* y = z + c * 32 + k * 4;
+                const float* y = z + k * 4;
                 const float2 a = __fadd2_rn(make_float2(y[0], y[1]), na);
                 const float2 b = __fadd2_rn(make_float2(y[2], y[3]), nb);
                 const float2 ea = make_float2(ex2(a.x), ex2(a.y)), eb = make_float2(ex2(b.x), ex2(b.y));
@@ -943,13 +945,13 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
                 p[2 * k] = pack2<__half>(ea.x, ea.y);
                 p[2 * k + 1] = pack2<__half>(eb.x, eb.y);
               }
-              tmem_st_pairs(s_at + c * kUnit8, p);
+              tmem_st_pairs(s_at, p);
+              tc_wait_st();
             }
-            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_ready[w * 2 + h]);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_ready[w * 2]);
         } else {
 #pragma unroll 1
           for (int h = 0; h * kUnit8 < n16; ++h) {
