@@ -1178,7 +1178,7 @@ bool encode8(CUtensorMap* m, const TreeParams& P, const void* base, int box) {
   const cuuint32_t bx[4] = {(cuuint32_t)P.dim, (cuuint32_t)box, 1, 1}, one[4] = {1, 1, 1, 1};
   // What a miss brings to L2: not more than a row, unless the rows of a head lie
   // together.  With 256 bytes, 128 K tokens of 8 heads cost 735 MB of DRAM reads
-  // for 491.
+  // for 490.
   const CUtensorMapL2promotion promotion = P.s_slot == P.dim ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
                                            : P.dim == 64     ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
                                                              : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
