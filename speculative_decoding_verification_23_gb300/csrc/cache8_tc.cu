@@ -764,7 +764,8 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
           uint32_t top = max_u16x2(max_u16x2(finite_size2(v.x, em), finite_size2(v.y, em)),
                                    max_u16x2(finite_size2(v.z, em), finite_size2(v.w, em)));
           top = max(top & 0xffffu, top >> 16);
-          const uint32_t peers = __activemask();
+          // a row's lanes, which come here together or not at all; other rows' may have left
+          const uint32_t peers = ((1u << PER) - 1u) << (lane & ~(PER - 1));
 #pragma unroll
           for (int z = PER / 2; z > 0; z >>= 1) top = max(top, __shfl_xor_sync(peers, top, z));
           const Exact16 s16 = exact16<T>(top);
