@@ -844,6 +844,8 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
               s_ph ^= 1u;
               if (!ok) break;
               tc_fence_after();
+            } else {
+              __syncwarp();  // one lane arrived for the first half by itself, and loads from tensor memory want all
             }
             if (any) {
               const uint32_t s_at = tmem + lanes + w * kTcKeys + h * kUnit8;
@@ -970,6 +972,8 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
               s_ph ^= 1u << h;
               if (!ok) break;
               tc_fence_after();
+            } else {
+              __syncwarp();  // as above
             }
             const uint32_t s_at = tmem + lanes + w * kTcKeys + h * kUnit8;
             if (any) {
