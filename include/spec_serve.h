@@ -89,8 +89,9 @@ int spec_window_attention(const spec_window_args *args, void *out, int64_t so_no
  *
  * of k_scale and of v_scale (strides in elements); its key is the bytes'
  * values times that scale.  Scales are not negative and at most 2^60; a
- * value's scale below 2^-60 counts as 0.  Slots past a request's length, and
- * scales of blocks past it, may hold anything. */
+ * value's scale below 2^-60 counts as 0, and bytes of NaN are NaN under any.
+ * Slots past a request's length, and scales of blocks past it, may hold
+ * anything. */
 typedef struct {
   void *k;
   void *v;

@@ -598,18 +598,20 @@ __global__ void __launch_bounds__(kC8TcThreads, 1)
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) v[c] = *reinterpret_cast<const uint4*>(src + ((uint32_t)(c << 4) ^ in_x));
           if (kv) {
-            // values past the end of a tile's keys, whatever the slots hold, are
-            // zero for the product, and so are those whose scale counts as 0
-            const bool zero = row >= valid || scales[tc & (kC8Tiles - 1)][row >> 4].w != 0.f;
-            if (__any_sync(0xffffffffu, zero || some)) {
+            // Values past the end of a tile's keys, whatever the slots hold, are
+            // zero for the product, and so are those whose scale counts as 0, but
+            // for NaN, which a weight of 0 leaves NaN.  Where some rows see a value
+            // and others do not, NaN are left out and added to the rows at the end.
+            const bool past = row >= valid, zero = scales[tc & (kC8Tiles - 1)][row >> 4].w != 0.f;
+            if (__any_sync(0xffffffffu, past || zero || some)) {
 #pragma unroll
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t* e = reinterpret_cast<uint32_t*>(&v[c]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const uint32_t nan = some ? __vcmpeq4(e[k] & 0x7f7f7f7fu, 0x7f7f7f7fu) : 0u;
-                  odd = odd || (nan != 0u && !zero);
-                  e[k] = zero ? 0u : e[k] & ~nan;
+                  const uint32_t nan = past ? 0u : __vcmpeq4(e[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                  odd = odd || (some && nan != 0u);
+                  e[k] &= past ? 0u : zero ? (some ? 0u : nan) : some ? ~nan : 0xffffffffu;
                 }
               }
             }
