@@ -160,8 +160,8 @@ int spec_cache8_attention(const spec_cache8_args *args, void *out, int64_t so_no
  * unless need > s; then `need` is its scale, and the bytes of its earlier
  * tokens become e4m3(value * s * (1 / need)).  In other blocks the scale is
  * `need`.  New bytes are e4m3(x * (1 / scale)), to nearest, ties to even (0 for
- * scale 0); infinities and NaN become NaN.  Slots of other tokens keep their
- * bytes.
+ * a scale below 2^-126, under which all new ones are 0); infinities and NaN
+ * become NaN.  Slots of other tokens keep their bytes.
  *
  * A page that gets tokens belongs to one request.  A request with a bad
  * length, a node outside its tree or a bad page gets its status and out_len -1,

@@ -373,7 +373,9 @@ __global__ void __launch_bounds__(kC8Threads, D <= 128 ? 2 : 1) commit8_kernel(c
     const float need = scale_for(big);
     const float old = n.old;
     const bool grown = begun && need > old;
-    const float s = begun && !grown ? old : need, inv = s == 0.f ? 0.f : 1.f / s;
+    // Of a scale below 2^-126, which a block only keeps where its new tokens are 0,
+    // the inverse may be infinite, and 0 times it NaN.
+    const float s = begun && !grown ? old : need, inv = s < 0x1p-126f ? 0.f : 1.f / s;
     if ((n.flags & 1) && wsub == 0 && lane == 0 && (!begun || grown)) *scale = s;
     // eight values under the scale
     auto bytes8 = [&](const uint4& x, bool odd) {
