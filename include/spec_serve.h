@@ -40,7 +40,9 @@ extern "C" {
  * the rounding of the result for positions below 2^28 in size.
  *
  * q or k may have 0 heads.  A result may take the place of its own input (the
- * same pointer and strides); other overlaps of results are refused. */
+ * same pointer and strides); other overlaps of results are refused, and so are
+ * results whose own rows or heads overlap (a stride of 0 over several, say: inputs
+ * may have it). */
 typedef struct {
   int32_t rows;
   int32_t heads_q, heads_k;

@@ -43,6 +43,17 @@ bool rows_overlap(const Rows& a, const Rows& b) {
   return d < a.bytes || d + b.bytes > a.row;
 }
 
+// Whether rows or heads of a result share memory: the one of smaller stride lies
+// within the other's.
+bool overlaps_itself(int rows, int heads, int dim, int64_t s_row, int64_t s_head) {
+  if (heads < 1 || (rows < 2 && heads < 2)) return false;
+  if (rows < 2) return s_head < dim;
+  if (heads < 2) return s_row < dim;
+  const bool heads_inside = s_head <= s_row;
+  const unsigned long long inner = heads_inside ? s_head : s_row, outer = heads_inside ? s_row : s_head;
+  return inner < (unsigned)dim || outer < inner * ((heads_inside ? heads : rows) - 1ull) + dim;
+}
+
 int check_side(const void* p, int heads, int64_t s_row, int64_t s_head) {
   if (heads == 0) return SPEC_OK;
   if (!p) return SPEC_ERR_NULL;
@@ -174,6 +185,9 @@ int spec_norm_rotate(const spec_rotate_args* a, void* out_q, int64_t oq_row, int
         oq(out_q, a->rows, a->heads_q, a->dim, oq_row, oq_head), ok(out_k, a->rows, a->heads_k, a->dim, ok_row, ok_head);
     const bool q_in_place = out_q == a->q && oq_row == a->sq_row && oq_head == a->sq_head;
     const bool k_in_place = out_k == a->k && ok_row == a->sk_row && ok_head == a->sk_head;
+    if (overlaps_itself(a->rows, a->heads_q, a->dim, oq_row, oq_head) ||
+        overlaps_itself(a->rows, a->heads_k, a->dim, ok_row, ok_head))
+      return SPEC_ERR_SHAPE;
     if ((!q_in_place && rows_overlap(oq, q)) || (!k_in_place && rows_overlap(ok, k)) || rows_overlap(oq, k) ||
         rows_overlap(ok, q) || rows_overlap(oq, ok))
       return SPEC_ERR_SHAPE;
