@@ -13,7 +13,8 @@
  *   spec_cache8_commit       writes the accepted path's (or a prompt's) keys
  *                            and values to such a cache.
  *
- * The conventions of spec_tree.h hold.
+ * The conventions of spec_tree.h hold; an 8-bit cache's scales are among what
+ * results that overlap it are refused for.
  */
 #ifndef SPEC_SERVE_H
 #define SPEC_SERVE_H

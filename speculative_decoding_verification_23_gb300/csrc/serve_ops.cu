@@ -76,6 +76,13 @@ int check_cache8(const spec_cache8& c) {
   return SPEC_OK;
 }
 
+// Whether results overlap the scales of `layers` layers from `first` on.
+bool scale_overlap(const spec_cache8& c, int first, int layers, std::initializer_list<Span> results) {
+  const long long n = (layers - 1) * c.c_layer + (c.num_pages - 1) * c.c_page + (c.page_size / c.block - 1) * c.c_block +
+                      (c.heads - 1) * c.c_head + 1;
+  return overlap(results, {{c.k_scale + first * c.c_layer, n}, {c.v_scale + first * c.c_layer, n}});
+}
+
 // The same call over a 16-bit cache, for the checks and parameters that both
 // have (offsets into the cache apart).
 spec_tree_args as_tree(const spec_cache8_args& a) {
@@ -270,8 +277,10 @@ int spec_cache8_attention(const spec_cache8_args* a, void* out, int64_t so_node,
   const sv::TreePlan plan = plan_cache8(a, rc ? kPlanSms : sms);
   const sv::TreeWorkspace W = sv::make_tree_workspace(a->B, plan.grid, plan.rows, a->cache.dim);
   if (ws_bytes < W.total) return SPEC_ERR_WORKSPACE;
+  if (tree_overlap(&t, out_lse, out_status) ||
+      scale_overlap(a->cache, a->layer, 1, {{out_lse, (long long)a->total_nodes * a->heads_q}, {out_status, a->B}}))
+    return SPEC_ERR_SHAPE;
   if (rc) return rc;
-  if (tree_overlap(&t, out_lse, out_status)) return SPEC_ERR_SHAPE;
   sv::Cache8Params C;
   std::memset(&C, 0, sizeof(C));
   fill_tree(C.t, &t, plan, W, out, so_node, so_head, out_lse, out_status, workspace);
@@ -310,15 +319,16 @@ int spec_cache8_commit(const spec_cache8_commit_args* a, int32_t* out_len, int32
         !mult8(a->sn_head))
       return SPEC_ERR_ALIGN;
   }
-  int sms = 0;
-  rc = sm_count(&sms);
-  if (rc) return rc;
   const long long lens = a->B;
   if (overlap({{out_len, lens}, {out_status, lens}},
               {{a->cu_nodes, lens + 1}, {a->path, lens * a->ld_path}, {a->path_len, lens},
                {a->block_table, lens * a->ld_table}, {out_len == a->ctx_len ? nullptr : a->ctx_len, lens}}) ||
-      overlap({{out_status, lens}}, {{a->ctx_len, lens}, {out_len, lens}}))
+      overlap({{out_status, lens}}, {{a->ctx_len, lens}, {out_len, lens}}) ||
+      scale_overlap(c, 0, c.layers, {{out_len, lens}, {out_status, lens}}))
     return SPEC_ERR_SHAPE;
+  int sms = 0;
+  rc = sm_count(&sms);
+  if (rc) return rc;
   sv::Commit8Params P;
   std::memset(&P, 0, sizeof(P));
   P.cu = a->cu_nodes;
