@@ -61,9 +61,11 @@ struct Run {
 // 16384 rows of 32 heads of 128 take 55 us with 8 and 68 with 4.
 //
 // The angle in turns is positions[r] f_i / 2 pi.  Its fraction is exact in
-// 64-bit fixed point: F_i = frac(f_i / 2 pi) 2^64 once per CTA, in fp64, and
-// the fraction of position times F_i is the low 64 bits of the product of
-// whole numbers.  In fp32 a position of 2^17 leaves 7 bits of the turn.
+// 64-bit fixed point: F_i = frac(f_i / 2 pi) 2^64 once per CTA, in two fp64 parts
+// (one would leave 2^-52 of a frequency of several turns, 2^-24 of a turn at a
+// position of 2^28), and the fraction of position times F_i is the low 64 bits of
+// the product of whole numbers.  In fp32 a position of 2^17 leaves 7 bits of the
+// turn.
 //
 // Bytes bound it, 2 read and 2 written a channel: 55 us are 4.9 TB/s, 72 % of the
 // copy rate, half of the traffic writes; one row of 16 heads takes 6.9 us, a
@@ -75,9 +77,13 @@ __global__ void __launch_bounds__(kRotWarps * 32) norm_rotate_kernel(const Rotat
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane % G, sub = lane / G;
   after_previous();
   for (int i = tid; i < P.rot / 2; i += kRotWarps * 32) {
-    double t = (double)P.inv_freq[i] * 0.15915494309189535;  // 1 / 2 pi
-    t -= floor(t);
-    turn[i] = (unsigned long long)(t * 18446744073709551616.0);
+    const float freq = P.inv_freq[i];
+    // |f| / 2 pi = t + rest, 1 / 2 pi in two parts and the product's own rounding
+    const double f = fabs((double)freq), t = f * 0.15915494309189535;
+    const double rest = fma(f, -9.839338337591243e-18, fma(f, 0.15915494309189535, -t));
+    const unsigned long long part = (unsigned long long)((t - floor(t)) * 18446744073709551616.0) +
+                                    (unsigned long long)(long long)(rest * 18446744073709551616.0);
+    turn[i] = freq < 0.f ? 0ull - part : part;
   }
   __syncthreads();
   const bool real = l < D / (2 * CH), turns = l < P.rot / (2 * CH);
