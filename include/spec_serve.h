@@ -39,7 +39,7 @@ extern "C" {
  * The others stay as normed.  Everything is fp32 and rounded once; angles are
  * reduced exactly (64-bit fractions of a turn), within 2^-24 of a turn beside
  * the rounding of the result for positions below 2^28 and frequencies below 2^20
- * in size.
+ * in size.  An infinite or NaN frequency makes its pairs NaN.
  *
  * q or k may have 0 heads.  A result may take the place of its own input (the
  * same pointer and strides); other overlaps of results are refused, and so are

@@ -76,8 +76,10 @@ __global__ void __launch_bounds__(kRotWarps * 32) norm_rotate_kernel(const Rotat
   __shared__ unsigned long long turn[D / 2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane % G, sub = lane / G;
   after_previous();
+  bool odd = false;  // a frequency that is no number: its pairs are NaN
   for (int i = tid; i < P.rot / 2; i += kRotWarps * 32) {
     const float freq = P.inv_freq[i];
+    odd = odd || !isfinite(freq);
     // |f| / 2 pi = t + rest, 1 / 2 pi in two parts and the product's own rounding
     const double f = fabs((double)freq), t = f * 0.15915494309189535;
     const double rest = fma(f, -9.839338337591243e-18, fma(f, 0.15915494309189535, -t));
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(kRotWarps * 32) norm_rotate_kernel(const Rotat
                                     (unsigned long long)(long long)(rest * 18446744073709551616.0);
     turn[i] = freq < 0.f ? 0ull - part : part;
   }
-  __syncthreads();
+  odd = __syncthreads_or(odd) != 0;
   const bool real = l < D / (2 * CH), turns = l < P.rot / (2 * CH);
   // this lane's two runs
   const int o0 = turns && !P.interleaved ? CH * l : 2 * CH * l;
@@ -107,6 +109,7 @@ __global__ void __launch_bounds__(kRotWarps * 32) norm_rotate_kernel(const Rotat
         const int i = (e * H + sub) % CH;
         const int frac = turns ? (int)((turn[CH * l + i] * pos) >> 32) : 0;  // of 2^32 a turn, nearest turn
         sincospif((float)frac * 4.656612873077393e-10f, &s[e], &c[e]);
+        if (odd && turns && !isfinite(P.inv_freq[CH * l + i])) s[e] = c[e] = NAN;
       }
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
