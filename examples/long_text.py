@@ -62,7 +62,7 @@ class LongTarget(Target):
         return logits, torch.stack(ks), torch.stack(vs)
 
 
-def generate(seed=0, requests=3, rounds=30, beams=4, depth=3, page=16, block=8, model=None):
+def generate(seed=0, requests=3, rounds=30, beams=4, depth=3, page=16, block=16, model=None):
     """Decodes `rounds` rounds greedily from one start token a request.  Returns the requests' tokens, the caches'
     lengths and the pages that the windowed layers hold at the end."""
     model = model or LongTarget(seed=seed, layers=4)

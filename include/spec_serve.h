@@ -114,6 +114,12 @@ typedef struct {
 /* spec_tree_attention (window 0) or spec_window_attention over such a cache.
  * Queries, drafted keys and values and results are of `dtype`.
  *
+ * Heads of 64 and 128 channels, with pages and blocks of a multiple of 16 tokens
+ * and a positive scale, go to the tensor-memory kernel, all else to warp tiles,
+ * which read the keys anew for every 16 query rows of a key head: 64 requests of
+ * up to 9 nodes over up to 8192 tokens, 28 / 4 heads of 128, take 467 us with
+ * blocks of 8 tokens and 116 with blocks of 16.
+ *
  * Products run on fp16 operands that hold the bytes' values, and queries and
  * drafted keys and values, exactly: bf16 rows are scaled by powers of two
  * first, and what is below 2^-31 of a query row's largest finite size, or of that
