@@ -129,7 +129,10 @@ typedef struct {
  * such product (at least 2^6 of 2^16, smallest step 2^-24), so with p_j =
  * exp(s_j - lse) an output is off by at most 2^-11 (1 + 2^-19) sum_j p_j |v_j|
  * and half a step of its own rounding, beside what fp32 sums and exponentials
- * add and 2^-31 of the largest p_j vs_j for every key. */
+ * add and 2^-31 of the largest p_j vs_j for every key.  Keys whose p_j vs_j (a
+ * scale that counts as 0: 2^-60) is below 2^-118 of the row's largest may be left
+ * out of the sum and of lse as well.  An infinity whose weight is that small gives
+ * the row an infinity or NaN. */
 typedef struct {
   int32_t B;
   int32_t total_nodes; /* cu_nodes[B]                                        */
@@ -166,7 +169,8 @@ int spec_cache8_attention(const spec_cache8_args *args, void *out, int64_t so_no
  * For every block of tokens and head that gets new ones, for keys and for
  * values alike: `need` is the smallest power of two, from 2^-126 on, whose
  * 448-fold reaches the largest finite size of the new tokens' channels (0 where
- * these are all 0).  A block that holds tokens before ctx_len keeps its scale s
+ * these are all 0; above 2^60, which attention's bounds end at, for sizes above
+ * 448 2^60).  A block that holds tokens before ctx_len keeps its scale s
  * unless need > s; then `need` is its scale, and the bytes of its earlier
  * tokens become e4m3(value * s * (1 / need)).  In other blocks the scale is
  * `need`.  New bytes are e4m3(x * (1 / scale)), to nearest, ties to even (0 for

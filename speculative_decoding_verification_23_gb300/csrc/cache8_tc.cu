@@ -215,20 +215,21 @@ __device__ __forceinline__ float4 c8_scale(float ks, float vs) {
 //   fragment, so all eight warps are at work where 128 rows would leave half of
 //   them idle.
 //   The softmax goes by halves of a tile, whose products begin as soon as its
-//   weights are there; by whole tiles the chains below take 120 us for 114, the
+//   weights are there; by whole tiles the chains below took 120 us for 114, the
 //   long contexts 132 for 134.
 // 16 requests with trees over up to 16384 tokens, 32 / 8 heads, cold: 16 nodes (64
 // rows) 109 / 117 / 139 us with ROWS 64 / 128 / 256, 32 nodes 117 and 143 with 128
 // and 256, 64 nodes 217 and 166.
 //
-// 64 ragged requests of up to 9 nodes over up to 8192 tokens take 114 us, trees of
-// up to 64 nodes over up to 16384 159, two requests over 128 K tokens 134 (54 % of
+// 64 ragged requests of up to 9 nodes over up to 8192 tokens take 115 us, trees of
+// up to 64 nodes over up to 16384 158, two requests over 128 K tokens 134 (54 % of
 // the copy rate).  A tile moves 208 KB through shared memory (32 written by the
 // copies, 32 read and 64 written by the conversion, 80 read by the products; 224
 // with more than 64 rows), 1650 cycles at 128 bytes a cycle, and takes some 2400:
 // the conversion works for 1500 of them and waits for copies and free slots for
-// the rest.  Products on the bytes themselves, with queries in three e4m3 parts,
-// took 195, 327 and 183 us.  A segment's end and the next one's queries cost some 20
+// the rest.  Scores on the bytes themselves, with queries in two 8-bit parts (bf16)
+// or three (fp16) and values converted as here, took 195, 327 and 183 us where this
+// kernel in its first form took 158, 194 and 178.  A segment's end and the next one's queries cost some 20
 // thousand cycles, which is what short contexts have besides.
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kC8TcThreads, 1)

@@ -46,7 +46,7 @@ __device__ __forceinline__ uint32_t without_nan8(uint32_t w, bool& any) {
 //
 // It serves the calls that the tensor-memory kernel does not take.  64 requests of
 // one token over up to 8192 tokens, 28 / 4 heads of 128, would take 160 us (125
-// there), and 9 nodes of them, five row tiles that read the keys anew, 470: the
+// there), and 9 nodes of them, five row tiles that read the keys anew, 467 (115): the
 // conversions and products of few rows bound it, not the copies.
 template <typename T, int D>
 __global__ void __launch_bounds__(kW8Warps * 32, W8Shape<D>::kCtas) cache8_warp_kernel(const Cache8Params C) {

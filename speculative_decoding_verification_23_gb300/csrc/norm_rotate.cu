@@ -67,9 +67,11 @@ struct Run {
 // the product of whole numbers.  In fp32 a position of 2^17 leaves 7 bits of the
 // turn.
 //
-// Bytes bound it, 2 read and 2 written a channel: 55 us are 4.9 TB/s, 72 % of the
-// copy rate, half of the traffic writes; one row of 16 heads takes 6.9 us, a
-// launch and two dependent loads.
+// Its bytes are 2 read and 2 written a channel: 55 us are 4.9 TB/s, 72 % of the
+// rate of a plain copy, which reads and writes as much.  The rest is each row's
+// start (position, sines, weights, nothing in flight yet) and the last pass: warps
+// take whole rows, 16384 of them 7 passes for 6.74.  One row of 16 heads takes 6.8
+// us, a launch and two dependent loads.
 template <typename T, int D, int CH>
 __global__ void __launch_bounds__(kRotWarps * 32) norm_rotate_kernel(const RotateParams P) {
   constexpr int G = kRotLanes<D, CH>, H = 32 / G;

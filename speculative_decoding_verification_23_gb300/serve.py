@@ -122,8 +122,8 @@ def make_rotate_args(*, q, k, positions, inv_freq, q_weight=None, k_weight=None,
 
 def spec_norm_rotate(args: SpecRotateArgs, *, out_q=None, out_k=None, stream=None):
     """Normed and rotated queries and keys through ``spec_norm_rotate``.  Returns (q [rows, heads_q, dim], k [rows,
-    heads_k, dim]), None for one that the block does not have.  Results may have any strides with a unit inner one;
-    they may be the inputs themselves."""
+    heads_k, dim]), None for one that the block does not have.  Results may have any strides with a unit inner one
+    and rows and heads that do not overlap; they may be the inputs themselves."""
     got = []
     for name, out, heads in (("out_q", out_q, args.heads_q), ("out_k", out_k, args.heads_k)):
         shape = (args.rows, heads, args.dim)
